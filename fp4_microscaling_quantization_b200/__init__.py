@@ -15,7 +15,8 @@ from ._lib import (FP4_MX_SCALE_CEIL, FP4_MX_SCALE_FLOOR, FP4_MXFP4, FP4_MXFP4_1
 
 __all__ = [
     "quantize", "dequantize", "gemm", "gemm_quantized", "linear", "linear_residual", "linear_workspace_size",
-    "quantize_sizes",
+    "quantize_sizes", "linear_w4a16", "KVCache", "kv_cache_sizes", "kv_append", "kv_gather", "paged_attention",
+    "paged_attention_workspace_size",
     "gemm_workspace_size", "check_device_status", "kernel_launches",
     "FP4_MXFP4", "FP4_NVFP4", "FP4_MXFP4_16", "FP4_ROUND_EVEN", "FP4_ROUND_AWAY", "FP4_MX_SCALE_CEIL",
     "FP4_MX_SCALE_FLOOR", "FP4_OUT_F32", "FP4_OUT_BF16", "FP4_SCALE_ABSMAX", "FP4_SCALE_MSE",
@@ -376,6 +377,205 @@ def linear_residual(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF1
          gscale.data_ptr() if gscale is not None else None, Wq.data_ptr(), Ws.data_ptr(), gW.data_ptr(), N,
          int(out_dtype), out.data_ptr(), out.stride(0), _stream_handle(torch, x.device))
     return out
+
+
+def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, out=None,
+                 weights_static: bool = False):
+    """The weight-only decode linear (M <= 16, see fp4_linear_w4a16): C = x W^T
+    with FP4 weights w = (Wq, Ws, gW) as for :func:`linear` and bf16
+    activations that are not quantized.  ``hadamard_k``: the rotation that w
+    was quantized with (x is rotated in the kernel)."""
+    import torch
+
+    fmt = _fmt(fmt)
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be a 2-D bf16 tensor, contiguous along K")
+    _dev(x, "x", None, torch.bfloat16, contiguous=False)
+    M, K = x.shape
+    N = w[0].shape[0]
+    Wq, Ws, gW = _operand(w, N, K, fmt, "W", x.device)
+    dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    else:
+        _out2d(out, M, N, dt, "out", x.device)
+    opts = _lib.Fp4Opts(0, 0, 0, 0, int(bool(weights_static)))
+    _run("fp4_linear_w4a16", x.device,
+         x.data_ptr(), M, K, x.stride(0) if M > 1 else (K + 7) // 8 * 8, fmt, int(hadamard_k), ctypes.byref(opts),
+         Wq.data_ptr(), Ws.data_ptr(), gW.data_ptr(), N, int(out_dtype), out.data_ptr(), out.stride(0) if M > 1 else N,
+         _stream_handle(torch, x.device))
+    return out
+
+
+# ---- the paged FP4 key-value cache ------------------------------------------
+def kv_cache_sizes(num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt) -> tuple[int, int]:
+    """Bytes of the elements and of the scales of K (and of V) of a cache."""
+    qb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _lib.check("fp4_kv_cache_sizes",
+               _lib.lib().fp4_kv_cache_sizes(num_pages, page_size, kv_heads, head_dim, _fmt(fmt), ctypes.byref(qb),
+                                             ctypes.byref(sb)))
+    return qb.value, sb.value
+
+
+class KVCache:
+    """One layer's paged key-value cache in FP4 (fp4_kv_cache).
+
+    ``k`` and ``v`` are (q, s, g) as elsewhere: q uint8 (num_pages, kv_heads,
+    page_size, head_dim / 2) packed nibbles, s uint8 (num_pages, kv_heads,
+    page_size, head_dim / block) scales, g a 1-element fp32 tensor (NVFP4's
+    tensor scale, static for the cache's life; not used by the other formats).
+    ``hadamard_k``: keys and values are held rotated by H_k.
+    A slot is page * page_size + position.  The tensors are checked here, once,
+    and must not be resized afterwards."""
+
+    def __init__(self, k, v, fmt, hadamard_k: int = 0):
+        import torch
+
+        fmt = _fmt(fmt)
+        if not isinstance(k[0], torch.Tensor) or k[0].dim() != 4:
+            raise ValueError("K elements must be a (num_pages, kv_heads, page_size, head_dim / 2) tensor")
+        pages, heads, page, half = k[0].shape
+        dev = k[0].device
+        qb, sb = kv_cache_sizes(pages, page, heads, 2 * half, fmt)
+        for name, (q, s, g) in (("K", k), ("V", v)):
+            _dev(q, name + " elements", dev, torch.uint8, qb)
+            _dev(s, name + " scales", dev, torch.uint8, sb)
+            _dev(g, name + " tensor scale", dev, torch.float32, 4)
+            if tuple(q.shape) != (pages, heads, page, half):
+                raise ValueError(f"{name} elements are {tuple(q.shape)}, K's {(pages, heads, page, half)}")
+        if hadamard_k not in (0, 16, 32, 64, 128) or (hadamard_k and 2 * half % hadamard_k):
+            raise ValueError("hadamard_k must be 0, 16, 32, 64 or 128 and divide head_dim")
+        self.k, self.v, self.fmt, self.hadamard_k = tuple(k), tuple(v), fmt, int(hadamard_k)
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, 2 * half
+        self.device = dev
+        self._c = _lib.Fp4KvCache(k[0].data_ptr(), k[1].data_ptr(), v[0].data_ptr(), v[1].data_ptr(), k[2].data_ptr(),
+                                  v[2].data_ptr(), pages, page, heads, 2 * half, fmt, int(hadamard_k))
+        self._p = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, head_dim: int, fmt, k_gscale: float = 1.0,
+              v_gscale: float = 1.0, hadamard_k: int = 0, device="cuda"):
+        """A zeroed cache.  ``k_gscale``, ``v_gscale``: NVFP4's tensor scales,
+        amax / 2688 of the keys and values to come (calibrated)."""
+        import torch
+
+        fmt = _fmt(fmt)
+        kv_cache_sizes(num_pages, page_size, kv_heads, head_dim, fmt)
+        shape = (num_pages, kv_heads, page_size)
+
+        def one(g):
+            return (torch.zeros(shape + (head_dim // 2,), dtype=torch.uint8, device=device),
+                    torch.zeros(shape + (head_dim // block_of(fmt),), dtype=torch.uint8, device=device),
+                    torch.full((1,), float(g), dtype=torch.float32, device=device))
+
+        return cls(one(k_gscale), one(v_gscale), fmt, hadamard_k)
+
+
+def _slots(slots, device):
+    import torch
+
+    _dev(slots, "slots", device, torch.int64)
+    if slots.dim() != 1:
+        raise ValueError("slots must be a 1-D int64 tensor")
+    return slots.shape[0]
+
+
+def kv_append(cache: KVCache, k, v, slots, round: int = FP4_ROUND_EVEN, mx_scale_rule: int = FP4_MX_SCALE_CEIL) -> None:
+    """Quantizes new tokens' keys and values (bf16, (tokens, kv_heads,
+    head_dim), contiguous along head_dim) into the cache at ``slots`` (int64).
+    Tokens whose slot is negative or past the cache are dropped; every other
+    token needs a slot of its own."""
+    import torch
+
+    tokens = _slots(slots, cache.device)
+    for name, t in (("k", k), ("v", v)):
+        _dev(t, name, cache.device, torch.bfloat16, contiguous=False)
+        if tuple(t.shape) != (tokens, cache.kv_heads, cache.head_dim) or (t.numel() and t.stride(2) != 1):
+            raise ValueError(f"{name} must be ({tokens}, {cache.kv_heads}, {cache.head_dim}), contiguous along its last axis")
+    opts = _lib.Fp4Opts(int(round), int(mx_scale_rule), 1, 0, 0)
+    many, heads = tokens > 1, cache.kv_heads > 1
+    _run("fp4_kv_append", cache.device,
+         cache._p, k.data_ptr(), k.stride(0) if many else 0, k.stride(1) if heads else 0, v.data_ptr(),
+         v.stride(0) if many else 0, v.stride(1) if heads else 0, slots.data_ptr(), tokens, ctypes.byref(opts),
+         _stream_handle(torch, cache.device))
+
+
+def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
+    """The keys and values at ``slots`` (int64), dequantized and turned back:
+    (k, v), each (tokens, kv_heads, head_dim).  A slot that is negative or past
+    the cache reads as zeros.  ``out`` = (k, v) reuses buffers."""
+    import torch
+
+    tokens = _slots(slots, cache.device)
+    dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    if out is None:
+        k = torch.empty(shape, dtype=dt, device=cache.device)
+        v = torch.empty(shape, dtype=dt, device=cache.device)
+    else:
+        k, v = out
+        for name, t in (("k", k), ("v", v)):
+            _dev(t, name, cache.device, dt, tokens * cache.kv_heads * cache.head_dim * (4 if dt == torch.float32 else 2))
+    _run("fp4_kv_gather", cache.device,
+         cache._p, slots.data_ptr(), tokens, int(out_dtype), k.data_ptr(), v.data_ptr(),
+         _stream_handle(torch, cache.device))
+    return k, v
+
+
+def paged_attention_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_seq_len: int,
+                                   window: int = 0) -> int:
+    b = ctypes.c_size_t()
+    _lib.check("fp4_paged_attention_workspace_size",
+               _lib.lib().fp4_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim, max_seq_len, window,
+                                                             ctypes.byref(b)))
+    return b.value
+
+
+def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | None = None, scale: float | None = None,
+                    window: int = 0, out_dtype: int = FP4_OUT_BF16, out=None, return_lse: bool = False, workspace=None):
+    """Attention of one new token per sequence over the paged FP4 cache (see
+    fp4_paged_attention): q (batch, q_heads, head_dim) bf16, page_table (batch,
+    pages) int32, seq_lens (batch,) int32, all on the device.
+
+    ``max_seq_len`` bounds the lengths on the host (default: what the table
+    reaches) and sizes the work split.  ``scale`` defaults to 1/sqrt(head_dim);
+    ``window`` > 0 attends to the last so many tokens.  Returns (batch,
+    q_heads, head_dim), with ``return_lse`` also the fp32 log-sum-exp of the
+    scores, (batch, q_heads)."""
+    import torch
+
+    dev = cache.device
+    _dev(q, "q", dev, torch.bfloat16, contiguous=False)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or (q.numel() and q.stride(2) != 1):
+        raise ValueError(f"q must be (batch, q_heads, {cache.head_dim}), contiguous along its last axis")
+    batch, heads = q.shape[0], q.shape[1]
+    _dev(page_table, "page_table", dev, torch.int32, contiguous=False)
+    if page_table.dim() != 2 or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be ({batch}, pages), contiguous along its rows")
+    _dev(seq_lens, "seq_lens", dev, torch.int32)
+    if tuple(seq_lens.shape) != (batch,):
+        raise ValueError(f"seq_lens must be ({batch},)")
+    cols = page_table.shape[1]
+    if max_seq_len is None:
+        max_seq_len = max(1, cols * cache.page_size)
+    dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
+    need = paged_attention_workspace_size(batch, heads, cache.kv_heads, cache.head_dim, max_seq_len, window)
+    if out is None:
+        out = torch.empty((batch, heads, cache.head_dim), dtype=dt, device=dev)
+    else:
+        _dev(out, "out", dev, dt, batch * heads * cache.head_dim * (4 if dt == torch.float32 else 2))
+    lse = torch.empty((batch, heads), dtype=torch.float32, device=dev) if return_lse else None
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _dev(workspace, "workspace", dev, torch.uint8)
+    _run("fp4_paged_attention", dev,
+         cache._p, q.data_ptr(), batch, heads, q.stride(0) if batch > 1 else 0, q.stride(1) if heads > 1 else 0,
+         page_table.data_ptr(), page_table.stride(0) if batch > 1 else cols, cols, seq_lens.data_ptr(), int(max_seq_len),
+         cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(out_dtype), out.data_ptr(),
+         lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
+         workspace.numel() if workspace is not None else 0, _stream_handle(torch, dev))
+    return (out, lse) if return_lse else out
 
 
 def kernel_launches() -> int:

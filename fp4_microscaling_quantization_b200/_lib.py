@@ -51,6 +51,13 @@ SIGNATURES = {
                           _vp, _sz, _vp]),
     "fp4_linear_residual": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64,
                                    _vp]),
+    "fp4_kv_cache_sizes": (_int, [_i64, _int, _int, _int, _int, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "fp4_kv_append": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "fp4_kv_gather": (_int, [_vp, _vp, _i64, _int, _vp, _vp, _vp]),
+    "fp4_paged_attention_workspace_size": (_int, [_i64, _int, _int, _int, _i64, _i64, ctypes.POINTER(_sz)]),
+    "fp4_paged_attention": (_int, [_vp, _vp, _i64, _int, _i64, _i64, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i64,
+                                   _int, _vp, _vp, _vp, _sz, _vp]),
+    "fp4_linear_w4a16": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64, _vp]),
     "fp4_kernel_launches": (ctypes.c_uint64, []),
     "fp4_test_inject_stall": (_int, [_int, ctypes.c_uint64]),
 }
@@ -59,6 +66,11 @@ SIGNATURES = {
 class Fp4Opts(ctypes.Structure):
     _fields_ = [("round", ctypes.c_int), ("mx_scale_rule", ctypes.c_int), ("gscale_given", ctypes.c_int),
                 ("scale_search", ctypes.c_int), ("weights_static", ctypes.c_int)]
+
+
+class Fp4KvCache(ctypes.Structure):
+    _fields_ = [("kq", _vp), ("ks", _vp), ("vq", _vp), ("vs", _vp), ("gk", _vp), ("gv", _vp), ("num_pages", _i64),
+                ("page_size", _int), ("kv_heads", _int), ("head_dim", _int), ("fmt", _int), ("hadamard_k", _int)]
 
 
 class Fp4Error(RuntimeError):

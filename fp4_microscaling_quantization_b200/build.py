@@ -11,6 +11,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,7 +22,7 @@ LIB = os.path.join(HERE, "libfp4.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-fmad=false", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
     "--expt-relaxed-constexpr",
     "-I", os.path.join(ROOT, "include"),
@@ -43,8 +45,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []), "-o", LIB + ".tmp", *sources()]
-    subprocess.check_call(cmd)
+    flags = [*NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else [])]
+    with tempfile.TemporaryDirectory() as tmp:  # the sources side by side, then one link
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in sources()]
+        with ThreadPoolExecutor(len(objs)) as pool:
+            list(pool.map(lambda so: subprocess.check_call([nvcc, *flags, "-c", "-o", so[1], so[0]]), zip(sources(), objs)))
+        subprocess.check_call([nvcc, *flags, "-shared", "-o", LIB + ".tmp", *objs])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

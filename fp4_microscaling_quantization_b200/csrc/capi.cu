@@ -6,7 +6,7 @@
 
 #include <atomic>
 
-#include "common.cuh"
+#include "kv.cuh"
 
 namespace fp4 {
 cudaError_t launch_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ld, int fmt,
@@ -39,6 +39,20 @@ cudaError_t launch_linear_fused(const uint16_t *x, int64_t ldx, int64_t M, int64
                                 int round_away, int mx_floor, const float *gA, const uint8_t *Wq, const uint8_t *Ws,
                                 const float *gW, int64_t N, int bf16out, void *C, int64_t ldc, int sms, cudaStream_t st,
                                 bool w_before_wait, bool residual, bool *taken);
+cudaError_t launch_kv_append(const KvView &c, int dim, int fmt, int hk, float ck, const uint16_t *k, int64_t k_tok,
+                             int64_t k_head, const uint16_t *v, int64_t v_tok, int64_t v_head, const int64_t *slots,
+                             int64_t tokens, int round_away, int mx_floor, cudaStream_t st, bool *too_many);
+cudaError_t launch_kv_gather(const KvView &c, int dim, int fmt, int hk, float ck, const int64_t *slots, int64_t tokens,
+                             int bf16out, void *k, void *v, cudaStream_t st, bool *too_many);
+size_t paged_attention_workspace_bytes(int64_t batch, int q_heads, int kv_heads, int dim, int64_t max_len, int64_t window,
+                                       int sms);
+cudaError_t launch_paged_attention(const KvView &c, int dim, int fmt, int hk, float ck, const uint16_t *q, int64_t batch,
+                                   int q_heads, int64_t q_b, int64_t q_h, const int32_t *table, int64_t table_b,
+                                   int64_t table_cols, const int32_t *lens, int64_t max_len, float scale, int64_t window,
+                                   int bf16out, void *out, float *lse, void *ws, int sms, cudaStream_t st);
+cudaError_t launch_linear_w4a16(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, int fmt, int hk, float ck,
+                                const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N, int bf16out, void *C,
+                                int64_t ldc, int w_early, int sms, cudaStream_t st);
 cudaError_t read_and_clear_device_errors(cudaStream_t st, unsigned int *err);
 static std::atomic<uint64_t> g_launches{0};
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -78,6 +92,46 @@ bool too_many_units(int64_t rows, int64_t cols) { return cols > 0 && rows > ((in
 // exact value, far inside half an fp32 ulp, so rounding it once to fp32 gives
 // the correctly rounded constant.
 float hadamard_constant(int k) { return k ? (float)(1.0 / sqrt((double)k)) : 1.0f; }
+
+// Sizes of a paged cache that the kernels take.
+fp4_status kv_geometry(int64_t num_pages, int page_size, int kv_heads, int head_dim, int fmt, int hadamard_k)
+{
+    if (num_pages < 0 || kv_heads < 1) return FP4_ERR_INVALID_ARG;
+    if (!valid_gemm_fmt(fmt) || !valid_k(hadamard_k)) return FP4_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+        return FP4_ERR_UNSUPPORTED;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP4_ERR_UNSUPPORTED;
+    if (hadamard_k && head_dim % hadamard_k) return FP4_ERR_UNSUPPORTED;
+    if (kv_heads > 65535 || num_pages > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+    return FP4_OK;
+}
+
+// The kernels' view of a cache.
+fp4_status kv_view(const fp4_kv_cache *cache, fp4::KvView &c)
+{
+    if (!cache) return FP4_ERR_INVALID_ARG;
+    const fp4_status st = kv_geometry(cache->num_pages, cache->page_size, cache->kv_heads, cache->head_dim, cache->fmt,
+                                      cache->hadamard_k);
+    if (st != FP4_OK) return st;
+    if (!cache->kq || !cache->ks || !cache->vq || !cache->vs) return FP4_ERR_INVALID_ARG;
+    if (cache->fmt == FP4_NVFP4 && (!cache->gk || !cache->gv)) return FP4_ERR_INVALID_ARG;
+    if (!aligned(cache->kq, 16) || !aligned(cache->ks, 16) || !aligned(cache->vq, 16) || !aligned(cache->vs, 16) ||
+        !aligned(cache->gk, 4) || !aligned(cache->gv, 4))
+        return FP4_ERR_ALIGNMENT;
+    int shift = 4;
+    while ((1 << shift) < cache->page_size) shift++;
+    c = {cache->kq, cache->ks, cache->vq, cache->vs, cache->gk, cache->gv, cache->num_pages, shift, cache->kv_heads};
+    return FP4_OK;
+}
+
+fp4_status attention_sizes(int64_t batch, int q_heads, int kv_heads, int head_dim, int64_t max_seq_len, int64_t window)
+{
+    if (batch < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || max_seq_len < 1 || window < 0)
+        return FP4_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP4_ERR_UNSUPPORTED;
+    if (batch > 65535 || q_heads > 65535 || max_seq_len > (1 << 30)) return FP4_ERR_UNSUPPORTED;
+    return FP4_OK;
+}
 
 }  // namespace
 
@@ -428,6 +482,134 @@ fp4_status fp4_nv_refine_gscale(const void *x, int64_t rows, int64_t cols, int64
     cudaError_t e = fp4::launch_nv_refine(static_cast<const uint16_t *>(x), rows, cols, ld_x, hadamard_k,
                                           hadamard_constant(hadamard_k), o.round == FP4_ROUND_AWAY, rounds, q, s,
                                           workspace, gscale, sm_count(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+fp4_status fp4_kv_cache_sizes(int64_t num_pages, int page_size, int kv_heads, int head_dim, int fmt, size_t *q_bytes,
+                              size_t *s_bytes)
+{
+    if (!q_bytes || !s_bytes) return FP4_ERR_INVALID_ARG;
+    const fp4_status st = kv_geometry(num_pages, page_size, kv_heads, head_dim, fmt, 0);
+    if (st != FP4_OK) return st;
+    const size_t rows = (size_t)num_pages * (size_t)kv_heads * (size_t)page_size;
+    *q_bytes = rows * (size_t)(head_dim / 2);
+    *s_bytes = rows * (size_t)(head_dim / (fmt == FP4_MXFP4 ? 32 : 16));
+    return FP4_OK;
+}
+
+fp4_status fp4_kv_append(const fp4_kv_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                         const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                         int64_t tokens, const fp4_opts *opts, void *stream)
+{
+    fp4_opts o = {FP4_ROUND_EVEN, FP4_MX_SCALE_CEIL, 0, FP4_SCALE_ABSMAX, 0};
+    if (opts) o = *opts;
+    fp4::KvView c;
+    fp4_status st = kv_view(cache, c);
+    if (st != FP4_OK) return st;
+    if (tokens < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0)
+        return FP4_ERR_INVALID_ARG;
+    if (o.round != FP4_ROUND_EVEN && o.round != FP4_ROUND_AWAY) return FP4_ERR_INVALID_ARG;
+    if (o.mx_scale_rule != FP4_MX_SCALE_CEIL && o.mx_scale_rule != FP4_MX_SCALE_FLOOR) return FP4_ERR_INVALID_ARG;
+    if (o.scale_search != FP4_SCALE_ABSMAX) return FP4_ERR_UNSUPPORTED;
+    if (tokens == 0) return FP4_OK;
+    if (!k || !v || !slots) return FP4_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_token_stride % 8 || k_head_stride % 8 || v_token_stride % 8 ||
+        v_head_stride % 8 || !aligned(slots, 8))
+        return FP4_ERR_ALIGNMENT;
+    bool too_many = false;
+    const cudaError_t e = fp4::launch_kv_append(
+        c, cache->head_dim, cache->fmt, cache->hadamard_k, hadamard_constant(cache->hadamard_k),
+        static_cast<const uint16_t *>(k), k_token_stride, k_head_stride, static_cast<const uint16_t *>(v), v_token_stride,
+        v_head_stride, slots, tokens, o.round == FP4_ROUND_AWAY, o.mx_scale_rule == FP4_MX_SCALE_FLOOR,
+        static_cast<cudaStream_t>(stream), &too_many);
+    if (too_many) return FP4_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+fp4_status fp4_kv_gather(const fp4_kv_cache *cache, const int64_t *slots, int64_t tokens, int out_dtype, void *k_out,
+                         void *v_out, void *stream)
+{
+    fp4::KvView c;
+    fp4_status st = kv_view(cache, c);
+    if (st != FP4_OK) return st;
+    if (tokens < 0) return FP4_ERR_INVALID_ARG;
+    if (out_dtype != FP4_OUT_F32 && out_dtype != FP4_OUT_BF16) return FP4_ERR_INVALID_ARG;
+    if (tokens == 0) return FP4_OK;
+    if (!slots || !k_out || !v_out) return FP4_ERR_INVALID_ARG;
+    if (!aligned(slots, 8) || !aligned(k_out, 32) || !aligned(v_out, 32)) return FP4_ERR_ALIGNMENT;
+    bool too_many = false;
+    const cudaError_t e = fp4::launch_kv_gather(c, cache->head_dim, cache->fmt, cache->hadamard_k,
+                                                hadamard_constant(cache->hadamard_k), slots, tokens,
+                                                out_dtype == FP4_OUT_BF16, k_out, v_out,
+                                                static_cast<cudaStream_t>(stream), &too_many);
+    if (too_many) return FP4_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv_heads, int head_dim,
+                                              int64_t max_seq_len, int64_t window, size_t *bytes)
+{
+    if (!bytes) return FP4_ERR_INVALID_ARG;
+    const fp4_status st = attention_sizes(batch, q_heads, kv_heads, head_dim, max_seq_len, window);
+    if (st != FP4_OK) return st;
+    *bytes = fp4::paged_attention_workspace_bytes(batch, q_heads, kv_heads, head_dim, max_seq_len, window, sm_count());
+    return FP4_OK;
+}
+
+fp4_status fp4_paged_attention(const fp4_kv_cache *cache, const void *q, int64_t batch, int q_heads,
+                               int64_t q_batch_stride, int64_t q_head_stride, const int32_t *page_table,
+                               int64_t table_stride, int64_t table_cols, const int32_t *seq_lens, int64_t max_seq_len,
+                               float scale, int64_t window, int out_dtype, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, void *stream)
+{
+    fp4::KvView c;
+    fp4_status st = kv_view(cache, c);
+    if (st != FP4_OK) return st;
+    st = attention_sizes(batch, q_heads, cache->kv_heads, cache->head_dim, max_seq_len, window);
+    if (st != FP4_OK) return st;
+    if (q_batch_stride < 0 || q_head_stride < 0 || table_cols < 0 || table_stride < 0) return FP4_ERR_INVALID_ARG;
+    if (table_cols > (1 << 30)) return FP4_ERR_UNSUPPORTED;
+    if (out_dtype != FP4_OUT_F32 && out_dtype != FP4_OUT_BF16) return FP4_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.0f)) return FP4_ERR_INVALID_ARG;  // NaN or infinite
+    if (batch == 0) return FP4_OK;
+    if (!q || !seq_lens || !out || (table_cols > 0 && !page_table)) return FP4_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || q_batch_stride % 8 || q_head_stride % 8 || !aligned(out, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(lse, 4))
+        return FP4_ERR_ALIGNMENT;
+    const int sms = sm_count();
+    const size_t need = fp4::paged_attention_workspace_bytes(batch, q_heads, cache->kv_heads, cache->head_dim, max_seq_len,
+                                                             window, sms);
+    if (need > 0 && (!workspace || ws_bytes < need)) return FP4_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, 16)) return FP4_ERR_ALIGNMENT;
+    const cudaError_t e = fp4::launch_paged_attention(
+        c, cache->head_dim, cache->fmt, cache->hadamard_k, hadamard_constant(cache->hadamard_k),
+        static_cast<const uint16_t *>(q), batch, q_heads, q_batch_stride, q_head_stride, page_table, table_stride,
+        table_cols, seq_lens, max_seq_len, scale, window, out_dtype == FP4_OUT_BF16, out, lse, workspace, sms,
+        static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
+                            const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,
+                            int out_dtype, void *C, int64_t ldc, void *stream)
+{
+    const int w_static = opts ? opts->weights_static : 0;
+    if (M < 0 || N < 0 || K < 0 || ld_x < K || ldc < N) return FP4_ERR_INVALID_ARG;
+    if (!valid_gemm_fmt(fmt)) return FP4_ERR_UNSUPPORTED;
+    if (out_dtype != FP4_OUT_F32 && out_dtype != FP4_OUT_BF16) return FP4_ERR_INVALID_ARG;
+    if (w_static != 0 && w_static != 1) return FP4_ERR_INVALID_ARG;
+    if (!valid_k(hadamard_k)) return FP4_ERR_UNSUPPORTED;
+    if (K % 32 || (hadamard_k && K % hadamard_k)) return FP4_ERR_UNSUPPORTED;
+    if (M > 16 || N > (1 << 30) || K > (1 << 30)) return FP4_ERR_UNSUPPORTED;  // the decode product only
+    if (M == 0 || N == 0) return FP4_OK;
+    if (K == 0) return FP4_ERR_UNSUPPORTED;
+    if (!x || !Wq || !Ws || !C) return FP4_ERR_INVALID_ARG;
+    if (fmt == FP4_NVFP4 && !gW) return FP4_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || (ld_x % 8) || !aligned(Wq, 16) || !aligned(Ws, 16) || !aligned(C, 16) || !aligned(gW, 4))
+        return FP4_ERR_ALIGNMENT;
+    const cudaError_t e = fp4::launch_linear_w4a16(
+        static_cast<const uint16_t *>(x), ld_x, M, K, fmt, hadamard_k, hadamard_constant(hadamard_k), Wq, Ws, gW, N,
+        out_dtype == FP4_OUT_BF16, C, ldc, w_static, sm_count(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 

@@ -372,6 +372,130 @@ fp4_status fp4_gemm_decode_noalloc(const uint8_t *Aq, const uint8_t *As, const f
                                    int64_t M, int64_t N, int64_t K, int fmt, int out_dtype,
                                    void *C, int64_t ldc, void *stream);
 
+/*
+ * ---- decode-time operators on FP4 data ---------------------------------------
+ *
+ * fp4_kv_cache — a paged key-value cache in FP4, one layer's.  The caller owns
+ * every buffer; the struct only names them.  K and V each hold
+ *   elements  (num_pages, kv_heads, page_size, head_dim / 2) bytes, packed as
+ *             fp4_quantize packs a row of head_dim values;
+ *   scales    (num_pages, kv_heads, page_size, head_dim / block) bytes, one per
+ *             block in order (rows, not the GEMM's tiles: attention reads them
+ *             with the tokens they belong to);
+ *   gk, gv    NVFP4: the tensor scale of all keys, of all values (one device
+ *             fp32 each, given: static for the cache's life).  Ignored for the
+ *             E8M0 formats, may be NULL.
+ * A slot is page * page_size + position in the page.
+ *   fmt         FP4_MXFP4 (block 32), FP4_NVFP4 or FP4_MXFP4_16 (block 16).
+ *   page_size   16, 32, 64, 128 or 256 tokens.
+ *   head_dim    64, 128 or 256.
+ *   hadamard_k  0, 16, 32, 64 or 128, head_dim % k == 0: keys and values are
+ *               held rotated by H_k along head_dim ("FP4 quantization analysis:
+ *               MXFP4 vs NVFP4" §3.2.3); every call below takes and returns
+ *               unrotated values.
+ *   kq, ks, vq, vs 16-byte aligned.  Errors: FP4_ERR_INVALID_ARG (null
+ *   pointers, negative sizes), FP4_ERR_UNSUPPORTED (fmt, page_size, head_dim,
+ *   hadamard_k outside these), FP4_ERR_ALIGNMENT.
+ */
+typedef struct {
+    uint8_t *kq, *ks, *vq, *vs;
+    const float *gk, *gv;
+    int64_t num_pages;
+    int page_size, kv_heads, head_dim, fmt, hadamard_k;
+} fp4_kv_cache;
+
+/* Bytes of kq (= of vq) and of ks (= of vs).  Host-only. */
+fp4_status fp4_kv_cache_sizes(int64_t num_pages, int page_size, int kv_heads, int head_dim, int fmt,
+                              size_t *q_bytes, size_t *s_bytes);
+
+/*
+ * fp4_kv_append — quantizes the keys and values of new tokens into their
+ * slots: fp4_quantize's arithmetic on each head row (H_k, absmax block
+ * scales, nearest rounding, given tensor scale), the same bits.
+ *   k, v    bf16, (tokens, kv_heads, head_dim): token and head strides in
+ *           elements, multiples of 8 and not negative; head_dim contiguous;
+ *           16-byte aligned.
+ *   slots   device int64[tokens], 8-byte aligned.  A token whose slot is
+ *           negative or past the cache (padding) is dropped.  Two tokens of a
+ *           call that name the same slot leave a mix of both in that slot, and
+ *           nothing else is touched: give every kept token a slot of its own.
+ *   opts    round and mx_scale_rule; may be NULL.  FP4_SCALE_MSE:
+ *           FP4_ERR_UNSUPPORTED.
+ * One launch.  tokens == 0 is a no-op.
+ */
+fp4_status fp4_kv_append(const fp4_kv_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                         const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                         int64_t tokens, const fp4_opts *opts, void *stream);
+
+/*
+ * fp4_kv_gather — tokens read back by their slots: fp4_dequantize's values
+ * (H_k applied again), the same bits.
+ *   slots      device int64[tokens]; one that is negative or past the cache
+ *              reads as zeros.  Slots may repeat.
+ *   out_dtype  FP4_OUT_F32 or FP4_OUT_BF16.
+ *   k_out, v_out  (tokens, kv_heads, head_dim), contiguous, 32-byte aligned.
+ * One launch.  tokens == 0 is a no-op.
+ */
+fp4_status fp4_kv_gather(const fp4_kv_cache *cache, const int64_t *slots, int64_t tokens, int out_dtype, void *k_out,
+                         void *v_out, void *stream);
+
+/* Bytes of scratch fp4_paged_attention needs (0 when none): by the sizes
+ * alone, the same value for the same arguments on one device type.  Host-only. */
+fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv_heads, int head_dim,
+                                              int64_t max_seq_len, int64_t window, size_t *bytes);
+
+/*
+ * fp4_paged_attention — attention of one new token per sequence over the
+ * paged FP4 cache: for query head h with key-value head h / (q_heads / kv_heads)
+ *   out = sum_t softmax_t(scale q . k_t) v_t
+ * over the live tokens t of sequence b: max(0, len - window) <= t < len
+ * (window 0: from 0), in pages whose table entry lies in [0, num_pages).
+ * Tokens of other entries (pages let go) take no part.  A sequence with no
+ * live token gets zeros, and lse = -inf.  k and v are the cache's dequantized
+ * values; what lies in a page past the length, NaN included, is not used.
+ *   q           bf16 (batch, q_heads, head_dim), strides in elements,
+ *               multiples of 8 and not negative; 16-byte aligned.
+ *   page_table  device int32, batch rows of table_cols entries, row stride
+ *               table_stride >= 0 elements: entry t / page_size holds token t.
+ *               Rows may share pages, or be one row (stride 0).
+ *   seq_lens    device int32[batch], tokens in the cache (the new one among
+ *               them, once appended).  A length above max_seq_len or above
+ *               table_cols * page_size is taken as the smaller of these, a
+ *               negative one as 0.
+ *   max_seq_len host bound of the lengths: it sizes the work split (1 .. 2^30).
+ *   scale       times the scores, 1/sqrt(head_dim) in most models.
+ *   out         (batch, q_heads, head_dim) contiguous, out_dtype, 16-byte aligned.
+ *   lse         fp32 (batch, q_heads): log sum_t exp(scale q . k_t); may be NULL.
+ *   workspace   fp4_paged_attention_workspace_size() bytes, 16-byte aligned
+ *               (NULL when that is 0); contents on entry do not matter.
+ * q_heads must be a multiple of kv_heads; batch and q_heads at most 65535.
+ * Sums and softmax statistics are fp32; weights enter the product with V as
+ * f16 (fp32 output: as two f16 terms), E8M0 scales more than 2^22 below the
+ * largest of their key (values: of the largest so far) count as zero.  One
+ * launch, or two where long sequences are cut; results repeat bit for bit.
+ */
+fp4_status fp4_paged_attention(const fp4_kv_cache *cache, const void *q, int64_t batch, int q_heads,
+                               int64_t q_batch_stride, int64_t q_head_stride, const int32_t *page_table,
+                               int64_t table_stride, int64_t table_cols, const int32_t *seq_lens, int64_t max_seq_len,
+                               float scale, int64_t window, int out_dtype, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/*
+ * fp4_linear_w4a16 — the weight-only linear layer of a decode step (M <= 16):
+ * C = H_k(x) W^T with FP4 weights and activations that stay in 16 bits, for
+ * layers whose activations do not stand the 4 bits of fp4_linear.
+ *   x, W, C, out_dtype, opts.weights_static   as fp4_linear; the other opts
+ *           are not used.  W as fp4_quantize wrote it, with the same hadamard_k.
+ * Unrotated activations are taken exactly (values more than 2^28 below their
+ * row's largest lose bits); rotated ones are rounded to 11 bits for bf16
+ * output and to 22 for fp32.  E8M0 scales more than 2^22 below the largest of
+ * their row's 128 elements count as zero.  fp32 sums in a fixed order.
+ * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch, no workspace.
+ */
+fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
+                            const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,
+                            int out_dtype, void *C, int64_t ldc, void *stream);
+
 /* Number of kernels this library has launched in this process so far
  * (host-side counter; diagnostics and launch accounting). */
 uint64_t fp4_kernel_launches(void);

@@ -1,0 +1,184 @@
+"""GPU tests of the weight-only decode linear against a plain 64-bit product
+of the dequantized weight and the (rotated) bf16 activations.
+
+Bounds.  Unrotated x and the scaled weights are exact f16 operands, so fp32
+output is off by the accumulation alone: K / 16 additions split over warps and
+CTAs, held to the library's product tolerance 1e-5 * sum |x| |w|.  Rotated x:
+hi + lo for fp32 output (2^-22) and the butterfly's fp32 (8 roundings, 2^-24),
+within the same; for bf16 output each value's f16 rounding adds 2^-11 of its
+term.  bf16 output: half a step, 2^-8 of the result.
+"""
+import pytest
+
+import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+MX, NV, MX16 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from fp4_microscaling_quantization_b200 import build
+    build.build()
+    import fp4_microscaling_quantization_b200 as m
+    return m
+
+
+def inputs(M, N, K, seed, size=0.02):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(M, K, generator=gen, device="cuda")
+    x[:, ::61] *= 20
+    w = torch.randn(N, K, generator=gen, device="cuda") * size
+    return x.to(torch.bfloat16), w.to(torch.bfloat16)
+
+
+def product64(x, W, fmt, hk, N, K):
+    """(C, sum |x| |w|) in the rotated domain, which leaves the product alone."""
+    q, s, g = W
+    s = s[ref.atoms_index(N, K // ref.block_of(fmt), s.device)]
+    w = ref.values64(q, s, fmt, g if fmt == NV else 1.0)
+    xr = ref.rotate64(x.double(), hk)
+    return xr @ w.T, xr.abs() @ w.abs().T
+
+
+def check(fp4, x, W, fmt, hk, N, **kw):
+    import torch
+    want, bound = product64(x, W, fmt, hk, N, x.shape[1])
+    got = fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, out_dtype=fp4.FP4_OUT_F32, **kw)
+    half = fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, **kw)
+    torch.cuda.synchronize()
+    off = (got.double() - want).abs()
+    assert (off <= 1e-5 * bound + 1e-30).all(), float((off / (bound + 1e-30)).max())
+    off = (half.double() - want).abs()
+    assert (off <= (1e-5 + (2.0**-11 if hk else 0)) * bound + 2.0**-8 * want.abs() + 1e-30).all()
+    return got
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 7, 8, 9, 15, 16])
+def test_rows(fp4, fmt, M):
+    x, w = inputs(M, 384, 1024, M)
+    check(fp4, x, fp4.quantize(w, fmt), fmt, 0, 384)
+
+
+# K tails of 32, one step, fewer steps than warps; N of one row, ragged tiles, many tiles
+SIZES = [(1, 1, 32), (16, 1, 32), (3, 127, 96), (5, 129, 160), (4, 200, 4064), (2, 1000, 128), (1, 128 * 150 + 3, 256),
+         (16, 300, 14336), (8, 64, 28704), (1, 4096, 4096)]
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_sizes(fp4, fmt, M, N, K):
+    x, w = inputs(M, N, K, 7)
+    check(fp4, x, fp4.quantize(w, fmt), fmt, 0, N)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("hk", [16, 32, 64, 128])
+@pytest.mark.parametrize("M,K", [(1, 128), (5, 1408), (16, 4096), (13, 14336)])
+def test_rotated(fp4, fmt, hk, M, K):
+    x, w = inputs(M, 320, K, hk + M)
+    check(fp4, x, fp4.quantize(w, fmt, hadamard_k=hk), fmt, hk, 320)
+
+
+def test_same_weight_as_the_quantizing_linear(fp4):
+    """One weight serves both decode linears; with activations that E2M1 holds
+    exactly they agree up to the sums' rounding."""
+    import torch
+    M, N, K = 4, 512, 2048
+    gen = torch.Generator().manual_seed(1)
+    x = torch.tensor(ref.GRID)[torch.randint(0, 8, (M, K), generator=gen)] * (1 - 2 * torch.randint(0, 2, (M, K), generator=gen))
+    x[:, ::32] = 6.0
+    x = x.to(torch.bfloat16).cuda()
+    _, w = inputs(M, N, K, 2)
+    W = fp4.quantize(w, MX)
+    a = fp4.linear(x, W, MX, out_dtype=fp4.FP4_OUT_F32)
+    _, bound = product64(x, W, MX, 0, N, K)
+    b = fp4.linear_w4a16(x, W, MX, out_dtype=fp4.FP4_OUT_F32)
+    assert ((a.double() - b.double()).abs() <= 2e-5 * bound).all()
+
+
+def test_strides_and_outputs(fp4):
+    """x as a view with a row stride, C inside a wider buffer; nothing else is written."""
+    import torch
+    M, N, K = 6, 260, 512
+    x, w = inputs(M, N, K + 64, 3)
+    W = fp4.quantize(w[:, :K].contiguous(), NV)
+    xv = x[:, 64:]
+    assert xv.stride(0) == K + 64
+    buf = torch.full((M + 1, N + 20), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = fp4.linear_w4a16(xv, W, NV, out=buf)
+    assert got is buf
+    assert torch.equal(buf[:M, :N], fp4.linear_w4a16(xv.contiguous(), W, NV))
+    assert (buf[M:] == 7).all() and (buf[:, N:] == 7).all()
+    check(fp4, xv, W, NV, 0, N)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_ends_of_the_range(fp4, fmt):
+    """Activations near bf16's largest and smallest, zero rows, rows far apart."""
+    import torch
+    x, w = inputs(5, 256, 512, 4)
+    x[0] = 0
+    x[1] *= 1e30
+    x[2] *= 1e-30
+    x[3, :] = 0
+    x[3, 77] = 2.0**100
+    check(fp4, x, fp4.quantize(w, fmt), fmt, 0, 256)
+
+
+def test_rows_of_far_apart_weights(fp4):
+    """E8M0: rows up to 2^100 apart, and blocks 2^16 apart in a row."""
+    import torch
+    x, w = inputs(3, 256, 1024, 5)
+    W = fp4.quantize(w, MX)
+    gen = torch.Generator().manual_seed(6)
+    s = (torch.randint(40, 140, (256, 1), generator=gen) + torch.randint(0, 17, (256, 32), generator=gen)).to(torch.uint8)
+    W[1][ref.atoms_index(256, 32)] = s.cuda()
+    check(fp4, x, W, MX, 0, 256)
+
+
+def test_padding_rows_reach_no_result(fp4):
+    """Scale rows past the weight's last may hold anything: NaN there."""
+    import torch
+    M, N, K = 2, 70, 128
+    x, w = inputs(M, N, K, 8)
+    for fmt in (NV, MX, MX16):
+        W = fp4.quantize(w, fmt)
+        want = fp4.linear_w4a16(x, W, fmt)
+        used = torch.zeros_like(W[1], dtype=torch.bool)
+        used[ref.atoms_index(N, K // ref.block_of(fmt)).cuda()] = True
+        W[1][~used] = 0x7F if fmt == NV else 0xFF
+        assert torch.equal(fp4.linear_w4a16(x, W, fmt), want)
+
+
+def test_weights_static_and_graph(fp4):
+    """Early weight loads give the same bits; captured and replayed with new x."""
+    import torch
+    x, w = inputs(4, 1024, 2048, 9)
+    W = fp4.quantize(w, NV, hadamard_k=64)
+    want = fp4.linear_w4a16(x, W, NV, hadamard_k=64)
+    torch.cuda.synchronize()
+    assert torch.equal(fp4.linear_w4a16(x, W, NV, hadamard_k=64, weights_static=True), want)
+    xin, out = torch.zeros_like(x), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fp4.linear_w4a16(xin, W, NV, hadamard_k=64, weights_static=True, out=out)
+        again = fp4.linear_w4a16(xin, W, NV, hadamard_k=64)
+    xin.copy_(x)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(again, want)
+
+
+def test_empty(fp4):
+    import torch
+    x, w = inputs(1, 128, 64, 10)
+    W = fp4.quantize(w, NV)
+    assert fp4.linear_w4a16(x[:0], W, NV).shape == (0, 128)

@@ -1,0 +1,266 @@
+"""GPU tests of attention over the paged FP4 cache against a plain 64-bit
+implementation of its formula (decode_ref.attention64, where the error bounds
+are derived).  fp32 output: within the bound; bf16 output: the weights' f16
+rounding (2^-11 of sum w |v|) and the output's own (2^-8) come on top.
+"""
+import math
+
+import pytest
+
+import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+MX, NV, MX16 = 0, 1, 2
+GK, GV = 0.037, 0.011
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from fp4_microscaling_quantization_b200 import build
+    build.build()
+    import fp4_microscaling_quantization_b200 as m
+    return m
+
+
+def make(fp4, fmt, dim, heads, page, hk, lens, seed, spread=4.0):
+    """A cache with every page written, shuffled pages in the table, and a page
+    of other tokens' data behind each sequence's last token."""
+    import torch
+    gen = torch.Generator().manual_seed(seed)
+    need = [max(1, -(-n // page)) for n in lens]
+    pages = sum(need) + 2
+    cache = fp4.KVCache.empty(pages, heads, page, dim, fmt, GK, GV, hk)
+    n = pages * page
+    x = torch.randn(2, n, heads, dim, generator=gen) * spread
+    x[:, :: 7] *= 0.01
+    x[0, :, :, ::13] *= 6
+    x = x.to(torch.bfloat16).cuda()
+    fp4.kv_append(cache, x[0], x[1], torch.arange(n, device="cuda"))
+    order = torch.randperm(pages, generator=gen).int()
+    table = torch.full((len(lens), max(need) + 1), 0, dtype=torch.int32)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    return cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+def query(batch, heads, dim, seed, size=1.0):
+    import torch
+    return (torch.randn(batch, heads, dim, generator=torch.Generator().manual_seed(seed)) * size).to(torch.bfloat16).cuda()
+
+
+def check(fp4, cache, q, table, lens, window=0, scale=None, **kw):
+    import torch
+    scale_ = cache.head_dim ** -0.5 if scale is None else scale
+    want, lse, err, mag = ref.attention64(q, cache.k[0], cache.k[1], cache.v[0], cache.v[1], cache.fmt, cache.k[2],
+                                          cache.v[2], cache.hadamard_k, table, lens, cache.page_size, scale_, window,
+                                          cache.num_pages)
+    got, l = fp4.paged_attention(q, cache, table, lens, scale=scale, window=window, out_dtype=fp4.FP4_OUT_F32,
+                                 return_lse=True, **kw)
+    half = fp4.paged_attention(q, cache, table, lens, scale=scale, window=window, **kw)
+    torch.cuda.synchronize()
+    tiny = 1e-30
+    off = (got.double() - want).abs()
+    assert (off <= err + tiny).all(), float((off / (err + tiny)).max())
+    off = (half.double() - want).abs()
+    assert (off <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + tiny).all()
+    # log-sum-exp: the scores' error (err / mag is above it), and the logarithm in fp32
+    fine = torch.isfinite(lse)
+    assert torch.equal(torch.isfinite(l), fine) and (l[~fine] == -math.inf).all()
+    rel = (err / mag.clamp(min=tiny)).amax(-1)
+    assert ((l.double() - lse).abs()[fine] <= (rel + 2.0**-21 * (1 + lse.abs()))[fine]).all()
+    return got
+
+
+FORMATS = [(f, d, k) for f in (MX, NV, MX16) for d in (64, 128, 256) for k in (0, d if d < 256 else 128)]
+
+
+@pytest.mark.parametrize("fmt,dim,hk", FORMATS)
+def test_formats_and_lengths(fp4, fmt, dim, hk):
+    """Every format, head size and rotation; lengths of 0, 1, page and step
+    borders, several steps of every warp."""
+    lens = [1, 0, 15, 16, 17, 31, 33, 64, 127, 200, 511, 700]
+    cache, table, n = make(fp4, fmt, dim, 2, 16, hk, lens, 1)
+    got = check(fp4, cache, query(len(lens), 8, dim, 2), table, n)
+    assert not got[1].any()
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 9, 12, 16, 17])
+@pytest.mark.parametrize("fmt,dim", [(NV, 128), (MX, 64)])
+def test_groups(fp4, group, fmt, dim):
+    """Any number of query heads to a key head, below and above one CTA's 8."""
+    cache, table, n = make(fp4, fmt, dim, 3, 32, 16, [70, 3], 3)
+    check(fp4, cache, query(2, 3 * group, dim, 4), table, n)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("fmt,dim", [(NV, 128), (MX, 256), (MX16, 64)])
+def test_pages(fp4, page, fmt, dim):
+    cache, table, n = make(fp4, fmt, dim, 2, page, 0, [page - 1, page, page + 1, 3 * page + 5], 5)
+    check(fp4, cache, query(4, 4, dim, 6), table, n)
+
+
+@pytest.mark.parametrize("fmt,dim,hk", [(NV, 128, 0), (MX, 128, 32), (MX16, 64, 0), (NV, 256, 0), (MX, 64, 64)])
+def test_long_sequences_are_cut_and_joined(fp4, fmt, dim, hk):
+    """Many chunks, uneven lengths (some end in the first chunk, one is empty)."""
+    lens = [9000, 1, 0, 513, 4096, 2047]
+    cache, table, n = make(fp4, fmt, dim, 1, 64, hk, lens, 7, spread=2.0)
+    assert fp4.paged_attention_workspace_size(len(lens), 4, 1, dim, 9000) > 0
+    check(fp4, cache, query(len(lens), 4, dim, 8), table, n, max_seq_len=9000)
+
+
+@pytest.mark.parametrize("window", [1, 16, 31, 100, 1000, 5000])
+@pytest.mark.parametrize("fmt", [NV, MX])
+def test_window(fp4, window, fmt):
+    cache, table, n = make(fp4, fmt, 64, 2, 16, 0, [1, 0, 40, 999, 2500], 9)
+    check(fp4, cache, query(5, 4, 64, 10), table, n, window=window)
+
+
+@pytest.mark.parametrize("fmt,dim", [(NV, 128), (MX, 64), (MX16, 256)])
+def test_missing_pages_take_no_part(fp4, fmt, dim):
+    """Entries outside the cache: single pages, a whole sequence."""
+    import torch
+    cache, table, n = make(fp4, fmt, dim, 2, 16, 0, [200, 90, 50, 1000], 11)
+    table[0, 1::3] = -1
+    table[0, 2] = 1 << 30
+    table[1, :] = cache.num_pages  # nothing left
+    table[2, :3] = torch.iinfo(torch.int32).min
+    got = check(fp4, cache, query(4, 6, dim, 12), table, n)
+    assert not got[1].any()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_what_lies_past_the_length_is_not_used(fp4, fmt, dim):
+    """NaN scales in every slot that takes no part."""
+    import torch
+    lens = [1, 17, 40, 600]
+    cache, table, n = make(fp4, fmt, dim, 1, 32, 0, lens, 13)
+    q = query(4, 2, dim, 14)
+    clean = fp4.paged_attention(q, cache, table, n, window=30)
+    live = torch.zeros(cache.num_pages * 32, dtype=torch.bool)
+    for b, m in enumerate(lens):
+        t = torch.arange(max(0, m - 30), m)
+        live[table[b].cpu().long()[t // 32] * 32 + t % 32] = True
+    dead = (~live).reshape(cache.num_pages, 32).cuda()
+    for s in (cache.k[1], cache.v[1]):
+        s[:, 0][dead] = 0x7F if fmt == NV else 0xFF
+    assert torch.equal(fp4.paged_attention(q, cache, table, n, window=30), clean)
+
+
+def test_live_nan_shows(fp4):
+    import torch
+    cache, table, n = make(fp4, NV, 64, 1, 16, 0, [40, 40], 15)
+    cache.v[1][int(table[0, 1]), 0, 3] = 0x7F
+    out = fp4.paged_attention(query(2, 2, 64, 16), cache, table, n)
+    assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+    cache, table, n = make(fp4, NV, 64, 1, 16, 0, [40, 40], 15)
+    cache.k[1][int(table[0, 1]), 0, 3] = 0x7F
+    out = fp4.paged_attention(query(2, 2, 64, 16), cache, table, n)
+    assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+
+
+def test_large_scores_and_tiny_queries(fp4):
+    """Scores of several hundred (one token takes all), queries near bf16's ends."""
+    for size in (300.0, 1e-30, 0.0):
+        cache, table, n = make(fp4, NV, 128, 1, 16, 0, [300], 17)
+        check(fp4, cache, query(1, 4, 128, 18, size), table, n)
+    cache, table, n = make(fp4, MX, 64, 1, 16, 0, [300], 17)
+    check(fp4, cache, query(1, 4, 64, 18, 3e37), table, n, scale=1e-37)
+
+
+def test_far_apart_scales(fp4):
+    """E8M0 scales over many binades: between tokens, and 2^20 within a row."""
+    import torch
+    cache, table, n = make(fp4, MX, 128, 1, 16, 0, [400], 19)
+    gen = torch.Generator().manual_seed(20)
+    cache.k[1].copy_(torch.randint(110, 128, cache.k[1].shape, generator=gen).to(torch.uint8))
+    cache.v[1].copy_(torch.randint(40, 128, cache.v[1].shape[:3] + (1,), generator=gen).to(torch.uint8).expand(cache.v[1].shape))
+    check(fp4, cache, query(1, 4, 128, 21, 0.3), table, n)
+
+
+def test_lengths_above_the_bounds(fp4):
+    """Above max_seq_len or the table's reach a length is cut; negative is empty."""
+    import torch
+    cache, table, n = make(fp4, NV, 64, 1, 16, 0, [64, 64, 64], 22)
+    q = query(3, 2, 64, 23)
+    want = fp4.paged_attention(q, cache, table[:, :3], torch.tensor([48, 48, 0], dtype=torch.int32, device="cuda"))
+    huge = torch.tensor([1 << 30, 49, -5], dtype=torch.int32, device="cuda")
+    assert torch.equal(fp4.paged_attention(q, cache, table[:, :3], huge), want)
+    assert torch.equal(fp4.paged_attention(q, cache, table, huge, max_seq_len=48), want)
+
+
+def test_strided_and_shared(fp4):
+    """Queries inside a fused projection, one table row for all sequences."""
+    import torch
+    cache, table, n = make(fp4, MX16, 128, 2, 16, 0, [100, 60, 100], 24)
+    qkv = query(3, 12, 128, 25)
+    q = qkv[:, 2:10]
+    row = table[:1].expand(3, -1)
+    assert row.stride(0) == 0
+    check(fp4, cache, q, row, n.clamp(max=100))
+    check(fp4, cache, qkv[:, ::3], table[:, :8], n)
+
+
+def test_repeats_bit_for_bit_on_streams(fp4):
+    """Two calls at once on two streams, each with its own workspace."""
+    import torch
+    cache, table, n = make(fp4, NV, 128, 1, 16, 0, [3000, 2000], 26)
+    q = query(2, 8, 128, 27)
+    want = fp4.paged_attention(q, cache, table, n)
+    torch.cuda.synchronize()
+    outs = []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(fp4.paged_attention(q, cache, table, n))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_decode_step_captured(fp4):
+    """Append and attention in one graph, replayed while the sequences grow, as
+    a decode loop uses them; two graphs share one workspace in one stream."""
+    import torch
+    B, H, G, D, page = 3, 2, 4, 64, 16
+    start = [30, 5, 600]
+    cache, _, _ = make(fp4, NV, D, H, page, 32, [700] * B, 28)
+    per = 44
+    table = torch.arange(B * per, dtype=torch.int32, device="cuda").reshape(B, per)
+    lens = torch.tensor(start, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+    k, v, q = (torch.zeros(B, n, D, dtype=torch.bfloat16, device="cuda") for n in (H, H, H * G))
+    ws = torch.empty(max(16, fp4.paged_attention_workspace_size(B, H * G, H, D, per * page)), dtype=torch.uint8, device="cuda")
+    out = [torch.empty(B, H * G, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+
+    def step(o):
+        fp4.kv_append(cache, k, v, slots)
+        fp4.paged_attention(q, cache, table, lens, out=o, workspace=ws)
+
+    step(out[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for o in out:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(o)
+        graphs.append(g)
+    gen = torch.Generator().manual_seed(29)
+    for i in range(6):
+        pos = lens.long()
+        slots.copy_(table.long().gather(1, (pos // page)[:, None])[:, 0] * page + pos % page)
+        lens += 1
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=gen).to(torch.bfloat16))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        want, _, err, mag = ref.attention64(q, cache.k[0], cache.k[1], cache.v[0], cache.v[1], NV, cache.k[2], cache.v[2],
+                                            32, table, lens, page, D ** -0.5, 0, cache.num_pages)
+        off = (out[i % 2].double() - want).abs()
+        assert (off <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + 1e-30).all()
