@@ -8,6 +8,7 @@ arithmetic runs in libfp4.so.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 from ._lib import (FP4_MX_SCALE_CEIL, FP4_MX_SCALE_FLOOR, FP4_MXFP4, FP4_MXFP4_16, FP4_NVFP4, FP4_OUT_BF16,
@@ -36,7 +37,7 @@ def _fmt(fmt) -> int:
 
 
 def _stream_handle(torch, device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _run(name: str, device, *args) -> None:
@@ -46,8 +47,17 @@ def _run(name: str, device, *args) -> None:
     stream the call is given."""
     import torch
 
+    if torch.cuda.current_device() == device.index:
+        _lib.check(name, getattr(_lib.lib(), name)(*args))
+        return
     with torch.cuda.device(device):
         _lib.check(name, getattr(_lib.lib(), name)(*args))
+
+
+@functools.lru_cache(maxsize=64)
+def _opts(round: int, mx_scale_rule: int, gscale_given: int, scale_search: int, weights_static: int):
+    """A pointer to an fp4_opts of these values (only ever read)."""
+    return ctypes.byref(_lib.Fp4Opts(round, mx_scale_rule, gscale_given, scale_search, weights_static))
 
 
 def _dev(t, name: str, device, dtype=None, min_bytes: int = 0, contiguous: bool = True):
@@ -65,8 +75,8 @@ def _dev(t, name: str, device, dtype=None, min_bytes: int = 0, contiguous: bool 
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() * t.element_size() < min_bytes:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {min_bytes} needed")
+    if min_bytes and t.nbytes < min_bytes:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, {min_bytes} needed")
     return t
 
 
@@ -91,7 +101,11 @@ def _out2d(out, rows: int, cols: int, dtype, name: str, device):
 
 
 def quantize_sizes(rows: int, cols: int, fmt) -> tuple[int, int]:
-    fmt = _fmt(fmt)
+    return _quantize_sizes(rows, cols, _fmt(fmt))
+
+
+@functools.lru_cache(maxsize=4096)
+def _quantize_sizes(rows: int, cols: int, fmt: int) -> tuple[int, int]:
     qb, sb = ctypes.c_size_t(), ctypes.c_size_t()
     _lib.check("fp4_quantize_sizes",
                _lib.lib().fp4_quantize_sizes(rows, cols, fmt, block_of(fmt), ctypes.byref(qb), ctypes.byref(sb)))
@@ -399,9 +413,9 @@ def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, 
         out = torch.empty((M, N), dtype=dt, device=x.device)
     else:
         _out2d(out, M, N, dt, "out", x.device)
-    opts = _lib.Fp4Opts(0, 0, 0, 0, int(bool(weights_static)))
     _run("fp4_linear_w4a16", x.device,
-         x.data_ptr(), M, K, x.stride(0) if M > 1 else (K + 7) // 8 * 8, fmt, int(hadamard_k), ctypes.byref(opts),
+         x.data_ptr(), M, K, x.stride(0) if M > 1 else (K + 7) // 8 * 8, fmt, int(hadamard_k),
+         _opts(0, 0, 0, 0, int(bool(weights_static))),
          Wq.data_ptr(), Ws.data_ptr(), gW.data_ptr(), N, int(out_dtype), out.data_ptr(), out.stride(0) if M > 1 else N,
          _stream_handle(torch, x.device))
     return out
@@ -492,12 +506,11 @@ def kv_append(cache: KVCache, k, v, slots, round: int = FP4_ROUND_EVEN, mx_scale
         _dev(t, name, cache.device, torch.bfloat16, contiguous=False)
         if tuple(t.shape) != (tokens, cache.kv_heads, cache.head_dim) or (t.numel() and t.stride(2) != 1):
             raise ValueError(f"{name} must be ({tokens}, {cache.kv_heads}, {cache.head_dim}), contiguous along its last axis")
-    opts = _lib.Fp4Opts(int(round), int(mx_scale_rule), 1, 0, 0)
     many, heads = tokens > 1, cache.kv_heads > 1
     _run("fp4_kv_append", cache.device,
          cache._p, k.data_ptr(), k.stride(0) if many else 0, k.stride(1) if heads else 0, v.data_ptr(),
-         v.stride(0) if many else 0, v.stride(1) if heads else 0, slots.data_ptr(), tokens, ctypes.byref(opts),
-         _stream_handle(torch, cache.device))
+         v.stride(0) if many else 0, v.stride(1) if heads else 0, slots.data_ptr(), tokens,
+         _opts(int(round), int(mx_scale_rule), 1, 0, 0), _stream_handle(torch, cache.device))
 
 
 def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
@@ -524,11 +537,20 @@ def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
 
 def paged_attention_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int, max_seq_len: int,
                                    window: int = 0) -> int:
+    """Scratch bytes of a paged_attention call of these sizes on the current device."""
     b = ctypes.c_size_t()
     _lib.check("fp4_paged_attention_workspace_size",
                _lib.lib().fp4_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim, max_seq_len, window,
                                                              ctypes.byref(b)))
     return b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_scratch(device: int, *sizes) -> int:
+    import torch
+
+    with torch.cuda.device(device):
+        return paged_attention_workspace_size(*sizes)
 
 
 def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | None = None, scale: float | None = None,
@@ -559,7 +581,7 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
     if max_seq_len is None:
         max_seq_len = max(1, cols * cache.page_size)
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
-    need = paged_attention_workspace_size(batch, heads, cache.kv_heads, cache.head_dim, max_seq_len, window)
+    need = _attention_scratch(dev.index, batch, heads, cache.kv_heads, cache.head_dim, int(max_seq_len), int(window))
     if out is None:
         out = torch.empty((batch, heads, cache.head_dim), dtype=dt, device=dev)
     else:

@@ -25,19 +25,21 @@
 //     are then the next product's B operand as they are: nothing is exchanged.
 //   * E2M1 times its block scale is exact in f16: for NVFP4 the E4M3 scale
 //     itself (6 significant bits, 2^-10 .. 2688), for E8M0 a power of two
-//     relative to the row's (K) or the running (V) largest scale.
+//     relative to the largest scale that the warp has met so far.
 //   * q in f16 as a power of two times hi + lo: query rows 0-7 of the product
 //     hold hi and rows 8-15 lo, so 22 bits cost nothing for groups of up to 8.
 //     Weights w_t are rounded to f16 (11 bits, scaled by 2^15 so that they
 //     stay normal down to 2^-29 of the largest; below, to steps of 2^-39), and
 //     for fp32 output are split into hi + lo as well, a second product.
-//   * Every warp streams its own steps of 16 or 32 tokens through its own ring
+//   * Every warp streams its own steps of 16, 32 or 64 tokens through its own ring
 //     of cp.async stages: no barrier among warps until their results are
 //     joined.  Rows lie swizzled, so all operand loads are free of bank conflicts.
 // Long sequences are cut into chunks of tokens over CTAs; a second kernel
 // joins the chunks.  The cut depends on the call's sizes only, and every sum
 // has a fixed order, so results repeat bit for bit.
 #include <math.h>
+
+#include <algorithm>
 
 #include "frag.cuh"
 #include "kv.cuh"
@@ -49,7 +51,9 @@ namespace attn {
 constexpr int NW = 4;           // warps per CTA, each on its own tokens
 constexpr int HT = 8;           // query heads per CTA
 constexpr float kPShift = 15.0f;  // weights are 2^15 w / w_max, inside f16's range
+constexpr int kAlign = 64;      // chunks start at multiples of the longest step
 constexpr int kMaxChunks = 1024;
+constexpr float kTiny = 1.17549435e-38f;  // the least normal number
 
 struct Args {
     KvView c;
@@ -57,15 +61,15 @@ struct Args {
     int64_t q_b, q_h;  // strides, elements
     const int32_t *table;
     int64_t table_b;       // row stride of the page table
-    int64_t table_tokens;  // tokens that a row of the table reaches
+    int table_tokens;      // tokens that a row of the table reaches (at most 2^30: lengths fit 31 bits)
     const int32_t *lens;
-    int64_t max_len;
-    int64_t window;        // 0 = none
+    int max_len;
+    int window;            // 0 = none
     int group, head_tiles, q_heads;
     float scale;           // times log2(e)
     float ck;
     int hk;
-    int64_t chunk;         // tokens per chunk, a multiple of 32
+    int chunk;             // tokens per chunk, a multiple of kAlign
     int chunks;
     void *out;
     float *lse;
@@ -77,13 +81,17 @@ template <int FMT, int D>
 struct Shape {
     static constexpr int SB = D / (FMT == FP4_MXFP4 ? 32 : 16);  // scale bytes per row
     static constexpr int QB = D / 2;                             // element bytes per row
-    static constexpr int TS = D == 256 ? 16 : 32;                // tokens per step
+    static constexpr int TS = D == 64 ? 64 : D == 128 ? 32 : 16; // tokens per step
     static constexpr int STAGE = 2 * TS * (QB + SB);             // bytes: K, V elements, K, V scales
-    static constexpr int ST = D == 64 ? 4 : 3;                   // stages per warp
+    static constexpr int ST = 3;                                 // stages per warp
     static constexpr int RING = NW * ST * STAGE;
     static constexpr int JOIN = NW * HT * D * 4;                 // the warps' results, over the ring
     static constexpr int QF = 2 * HT * D * 2;                    // hi and lo of q
-    static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + QF;
+    // q lies in warp 0's last stage, which its first loop trip fills, where it
+    // fits (dim 64, 128: a fourth CTA per SM), else behind the ring
+    static constexpr int BODY = RING > JOIN ? RING : JOIN;
+    static constexpr int QAT = QF <= STAGE ? (ST - 1) * STAGE : BODY;
+    static constexpr int SMEM = QF <= STAGE ? BODY : BODY + QF;
 };
 
 FP4_DEV float ex2(float x)
@@ -93,38 +101,13 @@ FP4_DEV float ex2(float x)
     return y;
 }
 
-// 16 bytes global -> shared, or 16 zero bytes.
-FP4_DEV void cp_async16(uint32_t dst, const void *src, bool live)
+// The transpose of an 8 x 8 matrix of 16-bit values held as a product's result
+// is (row lane / 4, columns 2 (lane % 4) and the next).
+FP4_DEV uint32_t transpose_8x8(uint32_t v)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-FP4_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-FP4_DEV void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-FP4_DEV void lds(uint32_t a, uint32_t *w, int n)
-{
-    if (n == 1)
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
-    else if (n == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-    else
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-}
-FP4_DEV uint32_t lds8(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("{\n\t.reg .u8 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u16.u8 %0, t;\n\t}" : "=h"(v) : "r"(a));
-    return v;
-}
-FP4_DEV uint32_t lds16(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
 // The token of column n in a tile of 8 (an involution).  Columns 2m and 2m+1
@@ -132,20 +115,19 @@ FP4_DEV uint32_t lds16(uint32_t a)
 // tokens 0, 3, 4, 7, for V's: both then touch every bank once.
 __host__ __device__ constexpr int tau(int n) { return n ^ ((n >> 1) & 1); }
 
-// Byte offset of 16-byte piece j of row t in the K and V element arrays of a stage.
+// Byte offset of 16-byte piece j of row t in the K and V element arrays of a
+// stage: as in the cache for dims 64 and 128 (V's loads then meet two rows in
+// a bank, which costs less than the addresses of a swizzle: they are immediate
+// offsets of one register); swizzled for dim 256, where it would be four.
 template <int D>
 FP4_DEV uint32_t k_piece(int t, int j)
 {
-    if (D == 64) return (uint32_t)((t ^ ((t >> 2) & 1)) * 32 + j * 16);
-    if (D == 128) return (uint32_t)(t * 64 + j * 16);
-    return (uint32_t)(t * 128 + (j ^ ((t & 1) << 2)) * 16);
+    return (uint32_t)(D == 256 ? t * 128 + (j ^ ((t & 1) << 2)) * 16 : t * (D / 2) + j * 16);
 }
 template <int D>
 FP4_DEV uint32_t v_piece(int t, int j)
 {
-    if (D == 64) return (uint32_t)((t ^ ((t >> 2) & 1)) * 32 + j * 16);
-    if (D == 128) return (uint32_t)(t * 64 + (j ^ (((t >> 2) & 1) << 1)) * 16);
-    return (uint32_t)(t * 128 + (j ^ (((t & 1) | (((t >> 2) & 1) << 1)) << 1)) * 16);
+    return (uint32_t)(D == 256 ? t * 128 + (j ^ (((t & 1) | (((t >> 2) & 1) << 1)) << 1)) * 16 : t * (D / 2) + j * 16);
 }
 
 // the same for two bytes, one in each half
@@ -157,17 +139,14 @@ FP4_DEV uint32_t e8m0_rel2(uint32_t e0, uint32_t e1, uint32_t ref)
 
 // The live range of a sequence's tokens, and where its chunks start.
 struct Range {
-    int64_t begin, end, base;
+    int begin, end, base;
 };
 FP4_DEV Range live_range(const Args &a, int b)
 {
     Range r;
-    int64_t n = a.lens[b];
-    n = n < a.max_len ? n : a.max_len;
-    n = n < a.table_tokens ? n : a.table_tokens;
-    r.end = n > 0 ? n : 0;
+    r.end = max(min(a.lens[b], min(a.max_len, a.table_tokens)), 0);
     r.begin = a.window > 0 && r.end > a.window ? r.end - a.window : 0;
-    r.base = r.begin & ~(int64_t)31;
+    r.base = r.begin & ~(kAlign - 1);
     return r;
 }
 
@@ -203,7 +182,9 @@ FP4_DEV void write_rows(const float *o, int rows, int64_t out_row, const Args &a
     }
 }
 
-template <int FMT, int D, int BF16OUT>
+// ROT: the cache is rotated, so q has more than f16's 11 bits and its lo rows
+// are not zero (a bf16 q is exact in the hi rows alone).
+template <int FMT, int D, int BF16OUT, bool ROT>
 __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const __grid_constant__ Args a)
 {
     using S = Shape<FMT, D>;
@@ -226,53 +207,89 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
     const int h0 = kvh * a.group + ht * HT;  // first query head
     const int nh = min(HT, a.group - ht * HT);
     const Range r = live_range(a, b);
-    const int64_t cs = r.base + chunk * a.chunk;
-    const int64_t ce = min(cs + a.chunk, r.end);
+    const int cs = r.base + chunk * a.chunk;  // below 2^31: the chunks cover max_len and less than one more
+    const int ce = min(cs + a.chunk, r.end);
     if (cs >= r.end && a.chunks > 1) return;  // the join reads no chunk past the length
 
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S::ST * S::STAGE);
     const int32_t *table = a.table + b * a.table_b;
-    const int pm = (1 << a.c.page_shift) - 1;
+    const uint32_t pm = (1u << a.c.page_shift) - 1u;
 
     // ---- the stream of this warp's steps ----
-    const int64_t first = cs + warp * S::TS;
-    auto page_at = [&](int64_t t) -> int { return t < ce ? __ldg(table + (t >> a.c.page_shift)) : -1; };
-    int next_page[HALVES];
+    // Page numbers of 32 half steps at a time, one per lane, loaded 32 ahead.
+    const int first = cs + warp * S::TS;
+    constexpr int PAGED = 32 / HALVES;  // steps per batch
+    auto pages_at = [&](int step) -> int {
+        const int t = first + (step + lane / HALVES) * (NW * S::TS) + 16 * (lane % HALVES);
+        return t < ce ? __ldg(table + (t >> a.c.page_shift)) : -1;
+    };
+    int page_now = pages_at(0), page_next = pages_at(PAGED);
+    uint32_t bad_now = __ballot_sync(0xFFFFFFFFu, (uint32_t)page_now >= (uint32_t)a.c.num_pages);  // num_pages < 2^31
+    if ((bad_now >> lane) & 1u) page_now = 0;
+    // this lane's pieces of a page: one 64-bit multiply-add per array and page
+    const uint32_t page_q = (uint32_t)(a.c.heads << a.c.page_shift) * S::QB, page_s = (uint32_t)(a.c.heads << a.c.page_shift) * S::SB;
+    const uint8_t *kq_lane = a.c.kq + (uint32_t)(kvh << a.c.page_shift) * S::QB + lane * 16;
+    const uint8_t *vq_lane = a.c.vq + (uint32_t)(kvh << a.c.page_shift) * S::QB + lane * 16;
+    const uint8_t *s_lane = (lane < 16 ? a.c.ks : a.c.vs) + (uint32_t)(kvh << a.c.page_shift) * S::SB + (lane & 15) * 16;
+    uint32_t k_dst[D == 256 ? PIECES / 2 : 1], v_dst[D == 256 ? PIECES / 2 : 1];  // dim 256: swizzled
 #pragma unroll
-    for (int h = 0; h < HALVES; h++) next_page[h] = page_at(first + 16 * h);
-    uint32_t holes = 0;  // bit 2 * stage + half: no page
-    auto fetch = [&](int64_t t0, int stage) {
-        const uint32_t dst = ring + (uint32_t)(stage * S::STAGE);
+    for (int i = 0; i < (D == 256 ? PIECES / 2 : 1); i++) {
+        const int p = i * 32 + lane, t = p / PIECES, j = p % PIECES;
+        k_dst[i] = ring + k_piece<D>(t, j);
+        v_dst[i] = ring + S::TS * S::QB + v_piece<D>(t, j);
+    }
+    const uint32_t s_dst = ring + 2 * S::TS * S::QB + (lane < 16 ? 0 : S::TS * S::SB) + (lane & 15) * 16;
+    const bool small_pages = (1 << a.c.page_shift) < S::TS;
+    uint32_t holes = 0;  // bit 4 * stage + half: no page
+    auto fetch = [&](int step, int stage) {
+        const int i0 = step % PAGED;
+        if (i0 == 0 && step) {
+            page_now = page_next;
+            page_next = pages_at(step + PAGED);
+            bad_now = __ballot_sync(0xFFFFFFFFu, (uint32_t)page_now >= (uint32_t)a.c.num_pages);
+            if ((bad_now >> lane) & 1u) page_now = 0;
+        }
+        const uint32_t bad = (bad_now >> (i0 * HALVES)) & ((1u << HALVES) - 1u);
+        holes = (holes & ~(15u << (4 * stage))) | (bad << (4 * stage));
+        const uint32_t so = (uint32_t)(stage * S::STAGE);
+        const uint32_t pos = (uint32_t)(first + step * (NW * S::TS)) & pm;
+        uint32_t page = __shfl_sync(0xFFFFFFFFu, page_now, i0 * HALVES);
+        const uint8_t *kq = kq_lane + (uint64_t)page * page_q + pos * S::QB, *vq = vq_lane + (uint64_t)page * page_q + pos * S::QB;
+        const uint8_t *sc = s_lane + (uint64_t)page * page_s + pos * S::SB;
 #pragma unroll
         for (int h = 0; h < HALVES; h++) {
-            const int page = next_page[h];
-            const bool live = (uint64_t)(int64_t)page < (uint64_t)a.c.num_pages;
-            holes = (holes & ~(1u << (2 * stage + h))) | ((live ? 0u : 1u) << (2 * stage + h));
-            next_page[h] = page_at(t0 + NW * S::TS + 16 * h);
-            const int64_t row = live ? ((((int64_t)page * a.c.heads + kvh) << a.c.page_shift) + ((t0 + 16 * h) & pm)) : 0;
-            const uint8_t *kq = a.c.kq + row * S::QB, *vq = a.c.vq + row * S::QB;
+            if (h > 0) {
+                if (small_pages) {  // a step of several pages
+                    page = __shfl_sync(0xFFFFFFFFu, page_now, i0 * HALVES + h);
+                    const uint32_t p = (pos + 16 * h) & pm;
+                    kq = kq_lane + (uint64_t)page * page_q + p * S::QB;
+                    vq = vq_lane + (uint64_t)page * page_q + p * S::QB;
+                    sc = s_lane + (uint64_t)page * page_s + p * S::SB;
+                } else {
+                    kq += 16 * S::QB;
+                    vq += 16 * S::QB;
+                    sc += 16 * S::SB;
+                }
+            }
+            const bool live = !((bad >> h) & 1u);
 #pragma unroll
             for (int i = 0; i < PIECES / 2; i++) {
-                const int p = i * 32 + lane, t = p / PIECES, j = p % PIECES;
-                cp_async16(dst + k_piece<D>(16 * h + t, j), kq + p * 16, live);
-                cp_async16(dst + S::TS * S::QB + v_piece<D>(16 * h + t, j), vq + p * 16, live);
+                cp_async16((D == 256 ? k_dst[i] : k_dst[0] + i * 512) + so + h * 16 * S::QB, kq + i * 512, live);
+                cp_async16((D == 256 ? v_dst[i] : k_dst[0] + S::TS * S::QB + i * 512) + so + h * 16 * S::QB, vq + i * 512, live);
             }
-            if ((lane & 15) < S::SB) {  // 16 rows' scales: SB pieces of K by the lower lanes, of V by the upper
-                const uint8_t *s = (lane < 16 ? a.c.ks : a.c.vs) + row * S::SB;
-                cp_async16(dst + 2 * S::TS * S::QB + (lane < 16 ? 0 : S::TS * S::SB) + h * 16 * S::SB + (lane & 15) * 16,
-                           s + (lane & 15) * 16, live);
-            }
+            if ((lane & 15) < S::SB)  // 16 rows' scales: SB pieces of K by the lower lanes, of V by the upper
+                cp_async16(s_dst + so + h * 16 * S::SB, sc, live);
         }
     };
 #pragma unroll
     for (int i = 0; i < S::ST - 1; i++) {
-        if (first + (int64_t)i * NW * S::TS < ce) fetch(first + (int64_t)i * NW * S::TS, i);
+        if (first + i * NW * S::TS < ce) fetch(i, i);
         cp_async_commit();
     }
 
     // ---- q: rotated, times a power of two that puts its largest value in
     // [2^14, 2^15), as f16 hi + lo in 16 rows of shared memory ----
-    uint16_t *qs = reinterpret_cast<uint16_t *>(smem + (S::SMEM - S::QF));
+    uint16_t *qs = reinterpret_cast<uint16_t *>(smem + S::QAT);
     for (int i = threadIdx.x; i < (HT * WPT < 32 ? 32 : HT * WPT); i += NW * 32) {  // whole warps: lanes exchange values
         const int h = i / WPT, u = i % WPT;
         uint4 raw[4] = {};
@@ -283,235 +300,271 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
         }
         float v[32];
         unpack_unit(raw, v);
-        rotate_unit(v, a.hk, a.ck, lane);
+        if (ROT) rotate_unit(v, a.hk, a.ck, lane);
         float amax = absmax_tree<32>(v);
 #pragma unroll
         for (int m = 1; m < WPT; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
         if (h >= HT) continue;
         int e = amax > 0.0f ? (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127 - 14 : 0;
         e = e < -126 ? -126 : e;  // 2^-e stays finite
-        const float down = exp2i(-e);
+        const float down = a.scale < 0.0f ? -exp2i(-e) : exp2i(-e);  // scores times a positive factor: their order holds
         if (u == 0) q_exp[h] = exp2i(e);
 #pragma unroll
         for (int j = 0; j < 16; j++) {
             const float x0 = __fmul_rn(v[2 * j], down), x1 = __fmul_rn(v[2 * j + 1], down);
             const uint32_t hi = pack_f16(x0, x1);
             const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
-            const uint32_t lo = pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
             reinterpret_cast<uint32_t *>(qs)[(h * D + u * 32) / 2 + j] = hi;
-            reinterpret_cast<uint32_t *>(qs)[((HT + h) * D + u * 32) / 2 + j] = lo;
+            if (ROT)
+                reinterpret_cast<uint32_t *>(qs)[((HT + h) * D + u * 32) / 2 + j] =
+                    pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
         }
     }
     __syncthreads();
-    uint32_t qf[2 * WPT][4];  // A operand: rows g (hi) and g + 8 (lo)
+    uint32_t qf[2 * WPT][ROT ? 4 : 2];  // B operand, column g: hi, then lo
 #pragma unroll
     for (int s = 0; s < 2 * WPT; s++) {
         const int w = s >> 1;
         const int e = (D == 256 ? ((w >> 2) * 4 + c) * 32 + (w & 3) * 8 : c * (D / 4) + w * 8) + (s & 1) * 4;
         const uint2 hi = *reinterpret_cast<const uint2 *>(qs + g * D + e);
-        const uint2 lo = *reinterpret_cast<const uint2 *>(qs + (HT + g) * D + e);
         qf[s][0] = hi.x;
-        qf[s][1] = lo.x;
-        qf[s][2] = hi.y;
-        qf[s][3] = lo.y;
+        qf[s][1] = hi.y;
+        if (ROT) {
+            const uint2 lo = *reinterpret_cast<const uint2 *>(qs + (HT + g) * D + e);
+            qf[s][ROT ? 2 : 0] = lo.x;
+            qf[s][ROT ? 3 : 1] = lo.y;
+        }
     }
-    float xscale = __fmul_rn(a.scale, q_exp[g]);
-    if (NV) xscale = __fmul_rn(xscale, *a.c.gk);
-    if (!NV) xscale = __fmul_rn(xscale, 0.00390625f);  // e8m0_rel's 2^8
+    __syncthreads();  // q's place becomes a stage
+    // Scores in units of log 2 are s * xs: xs > 0, so that a score of -inf stays one.
+    float xscale[2], xs[2];  // of heads 2c and 2c + 1
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        xscale[i] = __fmul_rn(__fmul_rn(fabsf(a.scale), q_exp[2 * c + i]), NV ? *a.c.gk : 0.00390625f);  // (E8M0: e8m0_rel's 2^8)
+        xs[i] = fmaxf(xscale[i], kTiny);
+    }
 
-    float m_run = -INFINITY, l_run = 0.0f;
-    uint32_t v_ref = 0;  // E8M0: the largest V scale byte so far
+    // where this lane's operands lie in a stage: tokens of other tiles follow at fixed distances
+    const uint32_t k_at = k_piece<D>(tau(g), D == 64 ? c >> 1 : c) + (D == 64 ? (c & 1) * 8 : 0);
+    const uint32_t k_at1 = D == 256 ? k_piece<D>(tau(g), 4 + c) : 0;
+    const uint32_t ks_at = 2 * S::TS * S::QB + tau(g) * S::SB + (FMT == FP4_MXFP4 ? (D == 64 ? c >> 1 : c) : D == 64 ? c : 2 * c);
+    const int vj = D == 64 ? g >> 2 : D == 128 ? g >> 1 : g, vb = D == 64 ? (g & 3) * 4 : D == 128 ? (g & 1) * 8 : 0;
+    const int vsj = FMT == FP4_MXFP4 ? vj : D == 64 ? g >> 1 : D == 128 ? g : 2 * g;
+    uint32_t v_at[2], vs_at[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        v_at[i] = S::TS * S::QB + v_piece<D>(tau(2 * c + i), vj) + vb;
+        vs_at[i] = 2 * S::TS * S::QB + S::TS * S::SB + tau(2 * c + i) * S::SB + vsj;
+    }
+
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+    uint32_t k_ref = 0, v_ref = 0;  // E8M0: the largest scale bytes so far
     float acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
 
-    int stage = 0;
-    for (int64_t t0 = first; t0 < ce; t0 += NW * S::TS) {
-        cp_async_wait<S::ST - 2>();
-        __syncwarp();
-        {
-            const int64_t tn = t0 + (int64_t)(S::ST - 1) * NW * S::TS;
-            const int sn = stage == 0 ? S::ST - 1 : stage - 1;  // the stage consumed last
-            if (tn < ce) fetch(tn, sn);
-            cp_async_commit();
-        }
-        const uint32_t kq = ring + (uint32_t)(stage * S::STAGE), vq = kq + S::TS * S::QB, ks = vq + S::TS * S::QB,
-                       vs = ks + S::TS * S::SB;
+    float x[NT / 2][4];  // 16 tokens: rows g and g + 8, heads 2c and 2c + 1 of each
+    uint32_t ph[NT], pl[NT];
+    constexpr int LW = (S::TS + 31) / 32;
+    uint32_t live[LW], ref_new = 0;  // a bit per token of the step, if not all take part
+    bool all = true;
 
-        // tokens of this step that take part
-        uint32_t live = 0xFFFFFFFFu;
-        if (t0 + S::TS > ce) live &= (1u << (int)(ce - t0)) - 1u;
-        if (t0 < r.begin) live &= 0xFFFFFFFFu << min((int)(r.begin - t0), 31);
-        if (t0 + 31 < r.begin) live = 0;
-        if ((holes >> (2 * stage)) & 1u) live &= 0xFFFF0000u;
-        if ((holes >> (2 * stage)) & 2u) live &= 0x0000FFFFu;
-        if (S::TS < 32) live |= 0xFFFFFFFFu << (S::TS % 32);
-        const bool all = live == 0xFFFFFFFFu;
-
-        // ---- scores ----
-        float x[NT][2];
+    // Before a step's scores: which of its tokens take part; E8M0: the largest
+    // scales so far (of V: to be taken up with the step's own weights).
+    auto look = [&](int t0, int stage) {
+        const uint32_t at = ring + (uint32_t)(stage * S::STAGE);
+        const uint32_t hole = (holes >> (4 * stage)) & 15u;
+        all = t0 + S::TS <= ce && t0 >= r.begin && !hole;
+        if (!all) {
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-            const int tk = n * 8 + tau(g);
-            uint32_t w[WPT], sc[(WPT + 1) / 2], ref = 0;
+            for (int i = 0; i < LW; i++) {
+                const int lo = r.begin - t0 - 32 * i, hi = ce - t0 - 32 * i;  // live from lo to hi
+                uint32_t v = hi >= 32 ? 0xFFFFFFFFu : hi > 0 ? (1u << hi) - 1u : 0u;
+                if (lo > 0) v = lo < 32 ? v & (0xFFFFFFFFu << lo) : 0u;
+                if ((hole >> (2 * i)) & 1u) v &= 0xFFFF0000u;
+                if ((hole >> (2 * i)) & 2u) v &= 0x0000FFFFu;
+                live[i] = v;
+                // whatever scales the others have (NaN among them) becomes 0
+                if (lane + 32 * i < S::TS && !((v >> lane) & 1u)) {
+                    const uint32_t ks = at + 2 * S::TS * S::QB + (lane + 32 * i) * S::SB;
 #pragma unroll
-            for (int p = 0; p < (D == 256 ? 2 : 1); p++)
-                lds(kq + k_piece<D>(tk, D == 64 ? c >> 1 : p * 4 + c) + (D == 64 ? (c & 1) * 8 : 0), w + 4 * p, D == 64 ? 2 : 4);
-            if (FMT == FP4_MXFP4) {  // one scale per 4 words (dim 64: shared by two lanes)
-                uint32_t e[D == 256 ? 2 : 1];
-#pragma unroll
-                for (int p = 0; p < (D == 256 ? 2 : 1); p++) e[p] = lds8(ks + tk * S::SB + (D == 64 ? c >> 1 : p * 4 + c));
-                ref = D == 256 ? max(e[0], e[D / 256]) : e[0];
-                ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 1));
-                ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 2));
-#pragma unroll
-                for (int i = 0; i < WPT / 2; i++) sc[i] = e8m0_rel(e[i >> 1], ref);
-            } else if (D == 64) {
-                const uint32_t e = lds8(ks + tk * S::SB + c);
-                if (NV) {
-                    sc[0] = e4m3x2_to_f16x2(e * 0x101u);
-                } else {
-                    ref = e;
-                    ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 1));
-                    ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 2));
-                    sc[0] = e8m0_rel(e, ref);
-                }
-            } else {
-                uint32_t e[D == 256 ? 2 : 1];
-#pragma unroll
-                for (int p = 0; p < (D == 256 ? 2 : 1); p++) e[p] = lds16(ks + tk * S::SB + (p * 4 + c) * 2);
-                if (NV) {
-#pragma unroll
-                    for (int p = 0; p < (D == 256 ? 2 : 1); p++) {
-                        const uint32_t f = e4m3x2_to_f16x2(e[p]);
-                        sc[2 * p] = __byte_perm(f, 0, 0x1010);
-                        sc[2 * p + 1] = __byte_perm(f, 0, 0x3232);
+                    for (int k = 0; k < S::SB; k += 2) {
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(ks + k), "h"((uint16_t)0) : "memory");
+                        asm volatile("st.shared.u16 [%0], %1;" ::"r"(ks + S::TS * S::SB + k), "h"((uint16_t)0) : "memory");
                     }
-                } else {
-                    ref = max(e[0] & 0xFF, e[0] >> 8);
-                    if (D == 256) ref = max(ref, max(e[D / 256] & 0xFF, e[D / 256] >> 8));
-                    ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 1));
-                    ref = max(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, 2));
-#pragma unroll
-                    for (int i = 0; i < WPT / 2; i++) sc[i] = e8m0_rel((e[i >> 1] >> (8 * (i & 1))) & 0xFF, ref);
                 }
             }
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < WPT; i++) {
-                uint32_t h[4];
-                e2m1x8_to_f16(w[i], h);
-#pragma unroll
-                for (int j = 0; j < 4; j++) h[j] = mul_f16x2(h[j], sc[i >> 1]);
-                mma_f16(s, qf[2 * i][0], qf[2 * i][1], qf[2 * i][2], qf[2 * i][3], h[0], h[1]);
-                mma_f16(s, qf[2 * i + 1][0], qf[2 * i + 1][1], qf[2 * i + 1][2], qf[2 * i + 1][3], h[2], h[3]);
-            }
-            // columns 2c and 2c + 1: hi and lo rows together
-            x[n][0] = __fmul_rn(__fadd_rn(s[0], s[2]), xscale);
-            x[n][1] = __fmul_rn(__fadd_rn(s[1], s[3]), xscale);
-            if (!NV) {  // times the rows' reference scales, which the lanes of those tokens hold
-                const uint32_t r0 = __shfl_sync(0xFFFFFFFFu, ref, 8 * c), r1 = __shfl_sync(0xFFFFFFFFu, ref, 8 * c + 4);
-                x[n][0] = __fmul_rn(x[n][0], exp2i((int)r0 - 127));
-                x[n][1] = __fmul_rn(x[n][1], exp2i((int)r1 - 127));
-            }
-            if (!all) {
-                if (!((live >> (n * 8 + tau(2 * c))) & 1u)) x[n][0] = -INFINITY;
-                if (!((live >> (n * 8 + tau(2 * c + 1))) & 1u)) x[n][1] = -INFINITY;
-            }
+            __syncwarp();
         }
-
-        // ---- running maximum ----
-        float mx = fmaxf(x[0][0], x[0][1]);
+        if (!NV) {
+            // bytes as pairs of 16-bit lanes; the rows of K, then those of V
+            constexpr int W = S::TS * S::SB / 4;  // words of each
+            uint32_t ek = 0, ev = 0;
 #pragma unroll
-        for (int n = 1; n < NT; n++) mx = fmaxf(mx, fmaxf(x[n][0], x[n][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const float m_new = fmaxf(m_run, mx);
-        uint32_t ref_new = v_ref;
-        if (!NV) {  // largest V scale of the step's live tokens
-            uint32_t e = 0;
-#pragma unroll
-            for (int i = 0; i < (S::TS * S::SB + 127) / 128; i++) {
+            for (int i = 0; i < (2 * W + 31) / 32; i++) {
                 const int w = i * 32 + lane;
-                if (w * 4 < S::TS * S::SB) {
-                    uint32_t q;
-                    lds(vs + w * 4, &q, 1);
-                    if (!all) {
-                        if (S::SB == 2) {
-                            if (!((live >> (2 * w)) & 1u)) q &= 0xFFFF0000u;
-                            if (!((live >> (2 * w + 1)) & 1u)) q &= 0x0000FFFFu;
-                        } else if (!((live >> (w * 4 / S::SB)) & 1u)) {
-                            q = 0;
-                        }
-                    }
-                    e = max(e, max_byte(q));
+                uint32_t q = 0;
+                if (2 * W % 32 == 0 || w < 2 * W) lds(at + 2 * S::TS * S::QB + w * 4, &q, 1);
+                const uint32_t e = __vmaxu2(q & 0x00FF00FFu, (q >> 8) & 0x00FF00FFu);
+                if (W % 32 == 0) {
+                    if (i * 32 < W) ek = __vmaxu2(ek, e);
+                    else ev = __vmaxu2(ev, e);
+                } else {
+                    ek = w < W ? __vmaxu2(ek, e) : ek;
+                    ev = w < W ? ev : __vmaxu2(ev, e);
                 }
             }
-            ref_new = max(v_ref, __reduce_max_sync(0xFFFFFFFFu, e));
-        }
-        if (__any_sync(0xFFFFFFFFu, m_new > m_run) || (!NV && ref_new != v_ref)) {
-            const float alpha = m_new > m_run ? ex2(__fsub_rn(m_run, m_new)) : 1.0f;  // 0 from -inf
-            l_run = __fmul_rn(l_run, alpha);
-            const float f = NV ? 1.0f : exp2i(max((int)v_ref - (int)ref_new, -127));
-            const float a0 = __fmul_rn(__shfl_sync(0xFFFFFFFFu, alpha, 8 * c), f);
-            const float a1 = __fmul_rn(__shfl_sync(0xFFFFFFFFu, alpha, 8 * c + 4), f);
+            const uint32_t k2 = k_ref * 0x10001u, v2 = ref_new * 0x10001u;
+            if (__any_sync(0xFFFFFFFFu, __vmaxu2(ek, k2) != k2 || __vmaxu2(ev, v2) != v2)) {
+                k_ref = max(k_ref, __reduce_max_sync(0xFFFFFFFFu, max(ek & 0xFFFFu, ek >> 16)));
+                ref_new = max(ref_new, __reduce_max_sync(0xFFFFFFFFu, max(ev & 0xFFFFu, ev >> 16)));
 #pragma unroll
-            for (int i = 0; i < MT; i++) {
-                acc[i][0] = __fmul_rn(acc[i][0], a0);
-                acc[i][1] = __fmul_rn(acc[i][1], a1);
-                acc[i][2] = __fmul_rn(acc[i][2], a0);
-                acc[i][3] = __fmul_rn(acc[i][3], a1);
-            }
-            m_run = m_new;
-            v_ref = ref_new;
-        }
-        const float off = __fsub_rn(m_run == -INFINITY ? 0.0f : m_run, kPShift);
-        uint32_t ph[NT], pl[NT];
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-            const float p0 = ex2(__fsub_rn(x[n][0], off)), p1 = ex2(__fsub_rn(x[n][1], off));
-            l_run = __fadd_rn(l_run, __fadd_rn(p0, p1));
-            ph[n] = pack_f16(p0, p1);
-            if (!BF16OUT) {
-                const __half2 hh = *reinterpret_cast<const __half2 *>(&ph[n]);
-                pl[n] = pack_f16(__fsub_rn(p0, __low2float(hh)), __fsub_rn(p1, __high2float(hh)));
+                for (int i = 0; i < 2; i++) xs[i] = fmaxf(__fmul_rn(xscale[i], exp2i((int)k_ref - 127)), kTiny);
             }
         }
 
-        // ---- values ----
+    };
+
+    // x = q . k of a step's tokens
+    auto scores = [&](int stage) {
+        const uint32_t at = ring + (uint32_t)(stage * S::STAGE);
 #pragma unroll
         for (int j = 0; j < NT / 2; j++) {
-            int tk[4] = {16 * j + tau(2 * c), 16 * j + tau(2 * c + 1), 16 * j + 8 + tau(2 * c), 16 * j + 8 + tau(2 * c + 1)};
-            uint32_t w[4][VW], s01[(VW + 1) / 2], s23[(VW + 1) / 2];
-            uint32_t e[4][(VW + 1) / 2];
+            uint32_t w[2][WPT], sc[2][(WPT + 1) / 2];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const int n = 2 * j + r;
+                lds(at + k_at + n * 8 * S::QB, w[r], D == 64 ? 2 : 4);
+                if (D == 256) lds(at + k_at1 + n * 8 * S::QB, w[r] + WPT / 2, 4);
+                const uint32_t ks = at + ks_at + n * 8 * S::SB;
+                if (FMT == FP4_MXFP4) {  // one scale per 4 words (dim 64: shared by two lanes)
+#pragma unroll
+                    for (int p = 0; p < (D == 256 ? 2 : 1); p++) {
+                        const uint32_t f = e8m0_rel(lds8(ks + 4 * p), k_ref);
+#pragma unroll
+                        for (int i = 0; i < (D == 64 ? 1 : 2); i++) sc[r][2 * p + i] = f;
+                    }
+                } else if (D == 64) {
+                    const uint32_t e = lds8(ks);
+                    sc[r][0] = NV ? e4m3x2_to_f16x2(e * 0x101u) : e8m0_rel(e, k_ref);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < D / 128; p++) {
+                        const uint32_t e = lds16(ks + 8 * p);
+                        if (NV) {
+                            const uint32_t f = e4m3x2_to_f16x2(e);
+                            sc[r][2 * p] = __byte_perm(f, 0, 0x1010);
+                            sc[r][2 * p + 1] = __byte_perm(f, 0, 0x3232);
+                        } else {
+                            sc[r][2 * p] = e8m0_rel(e & 0xFF, k_ref);
+                            sc[r][2 * p + 1] = e8m0_rel(e >> 8, k_ref);
+                        }
+                    }
+                }
+            }
+            x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WPT; i++) {
+                uint32_t h0[4], h1[4];
+                e2m1x8_to_f16(w[0][i], h0);
+                e2m1x8_to_f16(w[1][i], h1);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    h0[k] = mul_f16x2(h0[k], sc[0][i >> 1]);
+                    h1[k] = mul_f16x2(h1[k], sc[1][i >> 1]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    mma_f16(x[j], h0[2 * k], h1[2 * k], h0[2 * k + 1], h1[2 * k + 1], qf[2 * i + k][0], qf[2 * i + k][1]);
+                    if (ROT)
+                        mma_f16(x[j], h0[2 * k], h1[2 * k], h0[2 * k + 1], h1[2 * k + 1], qf[2 * i + k][ROT ? 2 : 0],
+                                qf[2 * i + k][ROT ? 3 : 1]);
+                }
+            }
+        }
+    };
+
+    // the step's weights, with everything so far on the new maxima
+    auto weights = [&]() {
+        if (!all) {
+#pragma unroll
+            for (int j = 0; j < NT / 2; j++) {
+                const uint32_t v = live[j / 2] >> (16 * (j & 1) + tau(g));
+                if (!(v & 1u)) x[j][0] = x[j][1] = -INFINITY;
+                if (!(v & 0x100u)) x[j][2] = x[j][3] = -INFINITY;
+            }
+        }
+        float m_new[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            float mx = fmaxf(x[0][i], x[0][2 + i]);
+#pragma unroll
+            for (int j = 1; j < NT / 2; j++) mx = fmaxf(mx, fmaxf(x[j][i], x[j][2 + i]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+            m_new[i] = fmaxf(m_run[i], __fmul_rn(mx, xs[i]));
+        }
+        if (__any_sync(0xFFFFFFFFu, m_new[0] > m_run[0] || m_new[1] > m_run[1]) || (!NV && ref_new != v_ref)) {
+            const float f = NV ? 1.0f : exp2i(max((int)v_ref - (int)ref_new, -127));
+            float alpha[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                alpha[i] = m_new[i] > m_run[i] ? ex2(__fsub_rn(m_run[i], m_new[i])) : 1.0f;  // 0 from -inf
+                l_run[i] = __fmul_rn(l_run[i], alpha[i]);
+                alpha[i] = __fmul_rn(alpha[i], f);
+                m_run[i] = m_new[i];
+            }
+#pragma unroll
+            for (int i = 0; i < MT; i++) {
+                acc[i][0] = __fmul_rn(acc[i][0], alpha[0]);
+                acc[i][1] = __fmul_rn(acc[i][1], alpha[1]);
+                acc[i][2] = __fmul_rn(acc[i][2], alpha[0]);
+                acc[i][3] = __fmul_rn(acc[i][3], alpha[1]);
+            }
+            v_ref = ref_new;
+        }
+        const float off0 = __fsub_rn(kPShift, m_run[0] == -INFINITY ? 0.0f : m_run[0]);
+        const float off1 = __fsub_rn(kPShift, m_run[1] == -INFINITY ? 0.0f : m_run[1]);
+#pragma unroll
+        for (int j = 0; j < NT / 2; j++) {
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float p0 = ex2(__fmaf_rn(x[j][2 * r], xs[0], off0)), p1 = ex2(__fmaf_rn(x[j][2 * r + 1], xs[1], off1));
+                l_run[0] = __fadd_rn(l_run[0], p0);
+                l_run[1] = __fadd_rn(l_run[1], p1);
+                const uint32_t h = pack_f16(p0, p1);
+                ph[2 * j + r] = transpose_8x8(h);  // head g, tokens of rows 2c and 2c + 1: V's B operand
+                if (!BF16OUT) {
+                    const __half2 hh = *reinterpret_cast<const __half2 *>(&h);
+                    pl[2 * j + r] = transpose_8x8(pack_f16(__fsub_rn(p0, __low2float(hh)), __fsub_rn(p1, __high2float(hh))));
+                }
+            }
+        }
+    };
+
+    auto values = [&](int stage) {
+        const uint32_t at = ring + (uint32_t)(stage * S::STAGE);
+#pragma unroll
+        for (int j = 0; j < NT / 2; j++) {
+            uint32_t w[4][VW], s01[(VW + 1) / 2], s23[(VW + 1) / 2], e[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                lds(vq + v_piece<D>(tk[i], D == 64 ? g >> 2 : D == 128 ? g >> 1 : g) + (D == 64 ? (g & 3) * 4 : D == 128 ? (g & 1) * 8 : 0), w[i], VW);
-                const bool on = all || ((live >> tk[i]) & 1u);
-                if (FMT == FP4_MXFP4) {
-                    e[i][0] = lds8(vs + tk[i] * S::SB + (D == 64 ? g >> 2 : D == 128 ? g >> 1 : g));
-                } else if (D == 256) {
-                    e[i][0] = lds16(vs + tk[i] * S::SB + 2 * g);
-                } else {
-                    e[i][0] = lds8(vs + tk[i] * S::SB + (D == 64 ? g >> 1 : g));
-                }
-                if (!on) e[i][0] = 0;
-                if (FMT != FP4_MXFP4 && D == 256) {
-                    e[i][VW / 4] = e[i][0] >> 8;
-                    e[i][0] &= 0xFF;
-                } else if (D == 256) {
-                    e[i][VW / 4] = e[i][0];
-                }
+                lds(at + v_at[i & 1] + (16 * j + 8 * (i >> 1)) * S::QB, w[i], VW);
+                const uint32_t vs = at + vs_at[i & 1] + (16 * j + 8 * (i >> 1)) * S::SB;
+                e[i] = FMT != FP4_MXFP4 && D == 256 ? lds16(vs) : lds8(vs);
             }
 #pragma unroll
             for (int k = 0; k < (VW + 1) / 2; k++) {
-                if (NV) {
-                    s01[k] = e4m3x2_to_f16x2(e[0][k] | (e[1][k] << 8));
-                    s23[k] = e4m3x2_to_f16x2(e[2][k] | (e[3][k] << 8));
+                const int sh = FMT == FP4_MXFP4 ? 0 : 8 * k;  // dim 256: both scales of a 16-bit load
+                if (NV && D == 256) {
+                    s01[k] = e4m3x2_to_f16x2(__byte_perm(e[0], e[1], k ? 0x0051 : 0x0040));
+                    s23[k] = e4m3x2_to_f16x2(__byte_perm(e[2], e[3], k ? 0x0051 : 0x0040));
+                } else if (NV) {
+                    s01[k] = e4m3x2_to_f16x2(e[0] | (e[1] << 8));
+                    s23[k] = e4m3x2_to_f16x2(e[2] | (e[3] << 8));
                 } else {
-                    // a dead token's byte 0 could still meet a reference of 0..22
-                    s01[k] = e8m0_rel2(e[0][k], e[1][k], v_ref);
-                    s23[k] = e8m0_rel2(e[2][k], e[3][k], v_ref);
+                    s01[k] = e8m0_rel2((e[0] >> sh) & 0xFF, (e[1] >> sh) & 0xFF, v_ref);
+                    s23[k] = e8m0_rel2((e[2] >> sh) & 0xFF, (e[3] >> sh) & 0xFF, v_ref);
                 }
             }
 #pragma unroll
@@ -533,57 +586,99 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
                 }
             }
         }
-        stage = stage == S::ST - 1 ? 0 : stage + 1;
+    };
+
+    // A step's scores are computed beside the values of the step before it: two
+    // independent chains for the scheduler.
+    if (first < ce) {
+        cp_async_wait<S::ST - 2>();
+        __syncwarp();
+        look(first, 0);
+        scores(0);
+        int stage = 0, step = 0;
+        for (int t0 = first + NW * S::TS; t0 < ce; t0 += NW * S::TS, step++) {
+            const int next = stage == S::ST - 1 ? 0 : stage + 1;
+            weights();
+            // into the stage of the step before this one, which all lanes have left
+            if (t0 + (S::ST - 2) * NW * S::TS < ce) fetch(step + S::ST - 1, stage == 0 ? S::ST - 1 : stage - 1);
+            cp_async_commit();
+            cp_async_wait<S::ST - 2>();  // the next step's copies
+            __syncwarp();
+            look(t0, next);
+            scores(next);
+            values(stage);
+            stage = next;
+        }
+        weights();
+        values(stage);
     }
 
     // ---- join the warps ----
-    l_run = __fadd_rn(l_run, __shfl_xor_sync(0xFFFFFFFFu, l_run, 1));
-    l_run = __fadd_rn(l_run, __shfl_xor_sync(0xFFFFFFFFu, l_run, 2));
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l_run[i] = __fadd_rn(l_run[i], __shfl_xor_sync(0xFFFFFFFFu, l_run[i], d));
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with the ring
     float *so = reinterpret_cast<float *>(smem) + warp * HT * D;
-    if (c == 0) {
-        sm_m[warp][g] = m_run;
-        sm_l[warp][g] = l_run;
+    if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            sm_m[warp][2 * c + i] = m_run[i];
+            sm_l[warp][2 * c + i] = l_run[i];
+        }
     }
     const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
 #pragma unroll
     for (int i = 0; i < MT; i++) {
         const int d = g * (D / 8) + 2 * i;
-        so[(2 * c) * D + d] = __fmul_rn(acc[i][0], vf);
-        so[(2 * c + 1) * D + d] = __fmul_rn(acc[i][1], vf);
-        so[(2 * c) * D + d + 1] = __fmul_rn(acc[i][2], vf);
-        so[(2 * c + 1) * D + d + 1] = __fmul_rn(acc[i][3], vf);
+        *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
+        *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
     }
     __syncthreads();
-    const float gv = NV ? *a.c.gv : 1.0f;
-    float *o = reinterpret_cast<float *>(smem);
-    for (int i = threadIdx.x; i < nh * D; i += NW * 32) {
-        const int h = i / D;
-        float m = sm_m[0][h];
+    if (threadIdx.x < nh) {  // the rows' factors, per warp
+        const int h = threadIdx.x;
+        float m = sm_m[0][h], l = 0.0f, f[NW];
 #pragma unroll
         for (int w = 1; w < NW; w++) m = fmaxf(m, sm_m[w][h]);
-        float s = 0.0f, l = 0.0f;
 #pragma unroll
         for (int w = 0; w < NW; w++) {
-            const float f = sm_m[w][h] == -INFINITY ? 0.0f : ex2(__fsub_rn(sm_m[w][h], m));
-            s = __fmaf_rn(f, o[w * HT * D + i], s);
-            l = __fmaf_rn(f, sm_l[w][h], l);
+            f[w] = sm_m[w][h] == -INFINITY ? 0.0f : ex2(__fsub_rn(sm_m[w][h], m));
+            l = __fmaf_rn(f[w], sm_l[w][h], l);
         }
         const int64_t row = (int64_t)b * a.q_heads + h0 + h;
+        float norm = 1.0f;
         if (a.chunks > 1) {
-            const int64_t p = row * a.chunks + chunk;
-            a.part_o[p * D + i % D] = s;
-            if (i % D == 0) a.part_ml[p] = make_float2(m, l);
+            a.part_ml[row * a.chunks + chunk] = make_float2(m, l);
         } else {
-            o[i] = l == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(s, l), gv);  // this thread's own element of warp 0's part
-            if (a.lse && i % D == 0)
-                a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
+            norm = l == 0.0f ? 0.0f : __fdiv_rn(NV ? *a.c.gv : 1.0f, l);
+            if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
         }
+#pragma unroll
+        for (int w = 0; w < NW; w++) sm_m[w][h] = __fmul_rn(f[w], norm);
+    }
+    __syncthreads();
+    float4 *o4 = reinterpret_cast<float4 *>(smem);
+    for (int i = threadIdx.x; i < nh * D / 4; i += NW * 32) {
+        const int h = i / (D / 4);
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            const float4 p = o4[w * (HT * D / 4) + i];
+            const float f = sm_m[w][h];
+            t.x = __fmaf_rn(f, p.x, t.x);
+            t.y = __fmaf_rn(f, p.y, t.y);
+            t.z = __fmaf_rn(f, p.z, t.z);
+            t.w = __fmaf_rn(f, p.w, t.w);
+        }
+        if (a.chunks > 1)
+            reinterpret_cast<float4 *>(a.part_o)[(((int64_t)b * a.q_heads + h0 + h) * a.chunks + chunk) * (D / 4) + i % (D / 4)] = t;
+        else
+            o4[i] = t;  // this thread's own element of warp 0's part
     }
     if (a.chunks > 1) return;
     __syncthreads();
-    write_rows<D, BF16OUT>(o, nh, (int64_t)b * a.q_heads + h0, a, NW * 32);
+    write_rows<D, BF16OUT>(reinterpret_cast<const float *>(smem), nh, (int64_t)b * a.q_heads + h0, a, NW * 32);
 }
 
 // Joins a row's chunks: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
@@ -649,44 +744,62 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
 }
 
 // ---------------------------------------------------------------------------
-// How a call is cut: tokens per chunk (a multiple of 32) and chunks per
+// How a call is cut: tokens per chunk (a multiple of kAlign) and chunks per
 // sequence, from its sizes alone (lengths live on the device).
 struct Plan {
     int64_t chunk;
     int chunks;
 };
 
-static Plan plan(int64_t batch, int kv_heads, int head_tiles, int64_t tokens, int sms)
+// The cheapest number of chunks by a model fitted to sweeps of chunk sizes on
+// the B200 (batch 1 x 262143 tokens to 64 x 8192, dims 64, 128, 256; time in
+// units of a warp's step): a CTA costs its warps' steps and 2.1 for its start
+// and end; whole rounds of the SMs' resident CTAs cost that each, a last round
+// that is partly filled 0.3 to 1 of it, a first one 0.6 to 1; joining n chunks
+// 0.6 + 0.02 n; in a batch, whose lengths differ as a rule, half a CTA more
+// (64 sequences of 1 to 8192 tokens: 4096 a chunk 98 us, 2048 88, 1024 88).
+// (One exact round for the long sequence: 75 us; 1.7 rounds of
+// half the chunk 79 us, 1.2 rounds 87 us.)
+static Plan plan(int64_t batch, int kv_heads, int head_tiles, int dim, int64_t tokens, int sms)
 {
-    const int64_t rows = batch * kv_heads * head_tiles;
-    int64_t want = ((int64_t)sms * 4 + rows - 1) / rows;  // CTAs for every resident slot
-    if (want < 1) want = 1;
-    int64_t chunk = (tokens + want - 1) / want;
-    if (chunk < 512) chunk = 512;
-    if (chunk > 2048) chunk = 2048;
-    int64_t chunks = (tokens + chunk - 1) / chunk;
-    if (chunks > kMaxChunks) {
-        chunk = (tokens + kMaxChunks - 1) / kMaxChunks;
+    const int64_t rows = batch * kv_heads * head_tiles, slots = (int64_t)sms * (dim == 256 ? 2 : 4);
+    const int64_t step = NW * (dim == 64 ? 64 : dim == 128 ? 32 : 16);
+    Plan best = {};
+    double least = 0.0;
+    const auto consider = [&](int64_t n) {
+        const int64_t chunk = ((tokens + n - 1) / n + kAlign - 1) / kAlign * kAlign;
+        n = (tokens + chunk - 1) / chunk;
+        const double t = 2.1 + (double)((chunk + step - 1) / step), rounds = (double)(rows * n) / (double)slots;
+        const double whole = floor(rounds), part = rounds - whole;
+        const double cost = t * ((rounds < 1.0 ? 0.6 + 0.4 * rounds : whole + (part > 0.0 ? 0.3 + 0.7 * part : 0.0)) + (batch > 1 ? 0.5 : 0.0)) +
+                            (n > 1 ? 0.6 + 0.02 * (double)n : 0.0);
+        if (best.chunks == 0 || cost < least) {
+            least = cost;
+            best = {chunk, (int)n};
+        }
+        return chunk > kAlign;
+    };
+    for (int64_t n = 1; n <= kMaxChunks && consider(n); n += 1 + n / 32) {
     }
-    chunk = (chunk + 31) / 32 * 32;
-    chunks = (tokens + chunk - 1) / chunk;
-    Plan p = {chunk, (int)(chunks < 1 ? 1 : chunks)};
-    return p;
+    for (int64_t r = 1; r <= 2; r++)  // whole rounds
+        if (r * slots / rows >= 1 && r * slots / rows <= kMaxChunks) consider(r * slots / rows);
+    return best;
 }
 
 // Tokens that a sequence's chunks have to cover: its live range from the last
-// multiple of 32 before it.
+// multiple of kAlign before it.
 static int64_t span(int64_t max_len, int64_t window)
 {
-    return window > 0 && max_len > window ? window + 31 : max_len;
+    return window > 0 && max_len > window ? window + kAlign - 1 : max_len;
 }
 
 template <int FMT, int D, int BF16OUT>
 static cudaError_t launch_t(const Args &a, int64_t batch, int kv_heads, cudaStream_t st)
 {
     using S = Shape<FMT, D>;
-    auto kern = paged_kernel<FMT, D, BF16OUT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    auto kern = a.hk ? paged_kernel<FMT, D, BF16OUT, true> : paged_kernel<FMT, D, BF16OUT, false>;
+    static std::atomic<uint64_t> done[2];
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), S::SMEM, done[a.hk ? 1 : 0]);
     if (e != cudaSuccess) return e;
     e = launch_k(kern, dim3((unsigned)(a.chunks * a.head_tiles), (unsigned)kv_heads, (unsigned)batch), dim3(NW * 32), S::SMEM, st, true, a);
     if (e != cudaSuccess || a.chunks == 1) return e;
@@ -710,7 +823,7 @@ static cudaError_t launch_f(const Args &a, int dim, int bf16out, int64_t batch, 
 size_t paged_attention_workspace_bytes(int64_t batch, int q_heads, int kv_heads, int dim, int64_t max_len, int64_t window, int sms)
 {
     const int tiles = (q_heads / kv_heads + attn::HT - 1) / attn::HT;
-    const attn::Plan p = attn::plan(batch > 0 ? batch : 1, kv_heads, tiles, attn::span(max_len, window), sms);
+    const attn::Plan p = attn::plan(batch > 0 ? batch : 1, kv_heads, tiles, dim, attn::span(max_len, window), sms);
     if (p.chunks == 1) return 0;
     return (size_t)batch * q_heads * p.chunks * ((size_t)dim + 2) * sizeof(float);
 }
@@ -727,18 +840,18 @@ cudaError_t launch_paged_attention(const KvView &c, int dim, int fmt, int hk, fl
     a.q_h = q_h;
     a.table = table;
     a.table_b = table_b;
-    a.table_tokens = table_cols << c.page_shift;
+    a.table_tokens = (int)std::min<int64_t>(table_cols << c.page_shift, int64_t(1) << 30);
     a.lens = lens;
-    a.max_len = max_len;
-    a.window = window;
+    a.max_len = (int)max_len;
+    a.window = (int)std::min<int64_t>(window, int64_t(1) << 30);
     a.group = q_heads / c.heads;
     a.head_tiles = (a.group + attn::HT - 1) / attn::HT;
     a.q_heads = q_heads;
     a.scale = (float)((double)scale * 1.4426950408889634);
     a.ck = ck;
     a.hk = hk;
-    const attn::Plan p = attn::plan(batch, c.heads, a.head_tiles, attn::span(max_len, window), sms);
-    a.chunk = p.chunk;
+    const attn::Plan p = attn::plan(batch, c.heads, a.head_tiles, dim, attn::span(max_len, window), sms);
+    a.chunk = (int)p.chunk;
     a.chunks = p.chunks;
     a.out = out;
     a.lse = lse;

@@ -79,4 +79,38 @@ FP4_DEV void rotate_unit(float *v, int hk, float ck, int lane)
     }
 }
 
+// 16 bytes global -> shared, or 16 zero bytes.
+FP4_DEV void cp_async16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+FP4_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+FP4_DEV void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+FP4_DEV void lds(uint32_t a, uint32_t *w, int n)
+{
+    if (n == 1)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(a));
+    else if (n == 2)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+    else
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+}
+FP4_DEV uint32_t lds8(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("{\n\t.reg .u8 t;\n\tld.shared.u8 t, [%1];\n\tcvt.u16.u8 %0, t;\n\t}" : "=h"(v) : "r"(a));
+    return v;
+}
+FP4_DEV uint32_t lds16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
 }  // namespace fp4

@@ -37,7 +37,11 @@ namespace fp4 {
 namespace w4 {
 
 constexpr int kThreads = 256;
-constexpr int kXBytes = 56 * 1024;  // shared memory for a stage of x: three CTAs per SM
+constexpr int kStep = 2560;                     // bytes of a warp's step: 32 rows x 64, and the scale words
+constexpr int kStages = 4;                      // steps of a warp's ring
+constexpr int kRing = 8 * kStages * kStep;
+constexpr int kMaxSmem = 224 * 1024;            // what a launch may ask for
+constexpr int kXBytes = 112 * 1024 - kRing;     // a stage of x: two CTAs per SM
 
 struct Args {
     const uint16_t *x;
@@ -57,22 +61,14 @@ struct Args {
     int w_early;          // W may be read before the grid-dependency wait
 };
 
-FP4_DEV uint4 ldg_stream(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 template <int FMT, int WR, int NT, int BF16OUT>
 __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constant__ Args a)
 {
     constexpr int WK = 8 / WR, ROWS = 32 * WR;
-    constexpr int PF = 2;  // steps in flight per warp
     constexpr bool NV = FMT == FP4_NVFP4;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float x_up[16];
-    __shared__ uint32_t top_w[16][8];
+    __shared__ uint32_t x_top[16];
     grid_dep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -83,53 +79,96 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
     const int r0 = (tile % (4 / WR)) * (8 * WR) + wr * 8 + g;  // row in the tile: r0 + 32 j
     const int s0 = (int)rank * a.slice, s1 = min(s0 + a.slice, a.chunks);  // K steps
 
-    const int64_t row_bytes = a.K / 2;
-    const uint8_t *wp = a.wq + (atom * 128 + r0) * row_bytes + c * 16;
+    // Nothing is predicated per row or lane: rows past N read row N - 1 (their
+    // results are not stored), elements past K the row's first (x is 0 there).
+    const uint32_t row_bytes = (uint32_t)(a.K / 2);
+    const uint8_t *wp[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) wp[j] = a.wq + min(atom * 128 + r0 + 32 * j, a.N - 1) * row_bytes;
     const uint8_t *sp = a.ws + (atom * a.nkb4 * 512 + r0 * 16);
-    bool row_in[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) row_in[j] = atom * 128 + r0 + 32 * j < a.N;
-
-    uint4 wn[PF][4], sn[PF];  // the coming steps' elements and scale words
+    // A lane's pieces of a step (4 rows' elements, their scale words) go through
+    // its own slots of a ring of asynchronous copies: no other lane waits.
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kStages * kStep) + lane * 16;
     auto load = [&](int step, int i) {
-        const bool in = step < s1 && (int64_t)step * 128 + c * 32 < a.K;
+        if (step < s1) {
+            uint32_t k = (uint32_t)step * 64 + c * 16;
+            k = k < row_bytes ? k : 0;
+            const uint32_t t = FMT == FP4_MXFP4 ? (uint32_t)step : min(2 * (uint32_t)step + (c >> 1), (uint32_t)a.nkb4 - 1);
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            wn[i][j] = in && row_in[j] ? ldg_stream(wp + 32 * j * row_bytes + (int64_t)step * 64) : make_uint4(0, 0, 0, 0);
-        const int64_t t = FMT == FP4_MXFP4 ? step : 2 * (int64_t)step + (c >> 1);
-        sn[i] = step < s1 && t < a.nkb4 ? ldg_stream(sp + t * 512) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < 4; j++) cp_async16(ring + i * kStep + j * 512, wp[j] + k, true);
+            cp_async16(ring + i * kStep + 2048, sp + (uint64_t)t * 512, true);
+        }
+        cp_async_commit();
     };
+    if (threadIdx.x < 16) x_top[threadIdx.x] = 0;
     if (!a.w_early) grid_dep_wait();
 #pragma unroll
-    for (int i = 0; i < PF; i++) load(s0 + wk + i * WK, i);
+    for (int i = 0; i < kStages - 1; i++) load(s0 + wk + i * WK, i);
     if (a.w_early) grid_dep_wait();
+    __syncthreads();
 
-    // ---- the slice's largest |x| per row: 8 / M warps a row, or two rows a warp ----
-    const int wpr = a.M < 8 ? 8 / a.M : 1;
-    {
+    // ---- the slice's largest |x| per row (after H_k where each thread holds
+    // its one unit of x; else before it, |H x| <= sqrt(k) max |x|) ----
+    const int units = (s1 - s0) * 4;  // 32-element units per row
+    const bool kept = a.M * units <= kThreads;
+    auto fetch_x = [&](int m, int64_t k, float *v) {
+        uint4 raw[4] = {};
+        if (m < a.M && k < a.K) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + k);
+#pragma unroll
+            for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
+        }
+        unpack_unit(raw, v);
+    };
+    // one unit (u of the stage) of row m to f16, in the order the lanes read it
+    const uint32_t xs = smem_u32(smem) + kRing;
+    const uint32_t pitch = (uint32_t)a.stage * 256 + 64;  // bytes per column: two columns' pieces fill all banks
+    auto put_x = [&](int m, int u, const float *v) {
+        const float up = x_up[m];
+        const float down = __uint_as_float((254u << 23) - __float_as_uint(up));  // its reciprocal
+        const uint32_t at = xs + m * pitch + (u >> 2) * 256 + (u & 3) * 16;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float x0 = __fmul_rn(v[8 * q + 2 * e], down), x1 = __fmul_rn(v[8 * q + 2 * e + 1], down);
+                hi[e] = pack_f16(x0, x1);
+                const __half2 hh = *reinterpret_cast<const __half2 *>(&hi[e]);
+                if (!BF16OUT) lo[e] = pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + q * 64), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+            if (!BF16OUT && a.cols > a.M)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + a.M * pitch + q * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+        }
+    };
+    float v[32];
+    const int mine_m = threadIdx.x / units, mine_u = threadIdx.x - mine_m * units;
+    if (kept) {
+        fetch_x(mine_m, (int64_t)s0 * 128 + mine_u * 32, v);
+        rotate_unit(v, a.hk, a.ck, lane);  // units of a row's step are 4 neighbouring lanes
+        if (mine_m < a.M) atomicMax(&x_top[mine_m], __float_as_uint(absmax_tree<32>(v)));
+    } else {
         const int64_t k0 = (int64_t)s0 * 128, k1 = min((int64_t)s1 * 128, a.K);
-        const int pieces = k1 > k0 ? (int)((k1 - k0) / 8) : 0;
+        const int pieces = (int)((k1 - k0) / 8), wpr = a.M < 8 ? 8 / a.M : 1;  // warps per row
         for (int m = warp / wpr; m < a.M; m += 8) {
             const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + k0);
             uint32_t top = 0;
 #pragma unroll 4
             for (int i = (warp % wpr) * 32 + lane; i < pieces; i += 32 * wpr) {
-                const uint4 v = __ldg(p + i);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint4 t = __ldg(p + i);
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                 for (int j = 0; j < 4; j++) top = max(top, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
             }
             top = __reduce_max_sync(0xFFFFFFFFu, top);
-            if (lane == 0) top_w[m][warp % wpr] = top;
+            if (lane == 0) atomicMax(&x_top[m], top);
         }
     }
     __syncthreads();
     if (threadIdx.x < a.M) {
-        uint32_t bits = 0;
-        for (int w = 0; w < wpr; w++) bits = max(bits, top_w[threadIdx.x][w]);
-        const float top = __uint_as_float(bits);
-        // |H x| <= sqrt(k) max |x|: 4 bits of room for a rotated row
-        int e = top > 0.0f ? (int)(__float_as_uint(top) >> 23) - 127 - (a.hk ? 10 : 14) : 0;
+        const uint32_t top = x_top[threadIdx.x];
+        int e = top ? (int)(top >> 23) - 127 - (a.hk && !kept ? 10 : 14) : 0;  // below 2^15 in f16
         e = e < -126 ? -126 : e;
         x_up[threadIdx.x] = exp2i(e);
     }
@@ -140,66 +179,33 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
 #pragma unroll
         for (int n = 0; n < NT; n++) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.0f;
 
-    const uint32_t xs = smem_u32(smem);
-    const uint32_t pitch = (uint32_t)a.stage * 256 + 64;  // bytes per column: two columns' pieces fill all banks
+    int slot = 0;
     for (int st = s0; st < s1; st += a.stage) {
         const int se = min(st + a.stage, s1);
         __syncthreads();  // scales are set; the last stage is consumed
-        // ---- x of this stage to f16, in the order the lanes read it ----
-        const int units = (se - st) * 4;
-        for (int i = threadIdx.x; i < (a.M * units + 31) / 32 * 32; i += kThreads) {
-            const int m = i / units, u = i - m * units;
-            const int64_t k = (int64_t)st * 128 + u * 32;
-            uint4 raw[4] = {};
-            const bool in = m < a.M;
-            if (in && k < a.K) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + k);
-#pragma unroll
-                for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
-            }
-            float v[32];
-            unpack_unit(raw, v);
-            rotate_unit(v, a.hk, a.ck, lane);  // units of a row's step are 4 neighbouring lanes
-            if (in) {
-                const float up = x_up[m];
-                const float down = __uint_as_float((254u << 23) - __float_as_uint(up));  // its reciprocal
-                const uint32_t at = xs + m * pitch + (u >> 2) * 256 + (u & 3) * 16;
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float x0 = __fmul_rn(v[8 * q + 2 * e], down), x1 = __fmul_rn(v[8 * q + 2 * e + 1], down);
-                        hi[e] = pack_f16(x0, x1);
-                        const __half2 hh = *reinterpret_cast<const __half2 *>(&hi[e]);
-                        lo[e] = pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
-                    }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + q * 64), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-                    if (a.cols > a.M)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + a.M * pitch + q * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
-                }
+        if (kept) {
+            if (mine_m < a.M) put_x(mine_m, mine_u, v);
+        } else {
+            const int n = (se - st) * 4;
+            for (int i = threadIdx.x; i < (a.M * n + 31) / 32 * 32; i += kThreads) {
+                const int m = i / n, u = i - m * n;
+                fetch_x(m, (int64_t)st * 128 + u * 32, v);
+                rotate_unit(v, a.hk, a.ck, lane);
+                if (m < a.M) put_x(m, u, v);
             }
         }
         __syncthreads();
 
-        // steps s0 + wk, s0 + wk + WK, ... (a stage is a multiple of WK steps)
+        // steps s0 + wk, s0 + wk + WK, ... (a stage of x is a multiple of WK steps)
         for (int step = st + wk; step < se; step += WK) {
-            uint32_t w[4][4], sc[4][2], ref[4];
+            cp_async_wait<kStages - 2>();
+            const uint32_t at = ring + slot * kStep;
+            load(step + (kStages - 1) * WK, slot == 0 ? kStages - 1 : slot - 1);  // the slot consumed last
+            slot = slot == kStages - 1 ? 0 : slot + 1;
+            uint32_t w[4][4], sw[4], sc[4][2], ref[4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                w[j][0] = wn[0][j].x;
-                w[j][1] = wn[0][j].y;
-                w[j][2] = wn[0][j].z;
-                w[j][3] = wn[0][j].w;
-            }
-            const uint32_t sw[4] = {sn[0].x, sn[0].y, sn[0].z, sn[0].w};
-#pragma unroll
-            for (int i = 0; i + 1 < PF; i++) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) wn[i][j] = wn[i + 1][j];
-                sn[i] = sn[i + 1];
-            }
-            load(step + PF * WK, PF - 1);
+            for (int j = 0; j < 4; j++) lds(at + j * 512, w[j], 4);
+            lds(at + 2048, sw, 4);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 if (FMT == FP4_MXFP4) {
@@ -219,13 +225,13 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
                     }
                 }
             }
+            // the step's own sums: added below with a rounding to nearest, which
+            // the product's accumulation of many steps would not give
             float part[2][NT][4];
-            if (!NV) {
 #pragma unroll
-                for (int t = 0; t < 2; t++)
+            for (int t = 0; t < 2; t++)
 #pragma unroll
-                    for (int n = 0; n < NT; n++) part[t][n][0] = part[t][n][1] = part[t][n][2] = part[t][n][3] = 0.0f;
-            }
+                for (int n = 0; n < NT; n++) part[t][n][0] = part[t][n][1] = part[t][n][2] = part[t][n][3] = 0.0f;
             const uint32_t xb = xs + (step - st) * 256 + c * 16;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -243,29 +249,28 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(bx[0]), "=r"(bx[1]), "=r"(bx[2]), "=r"(bx[3]) : "r"(xb + (8 * n + g) * pitch + i * 64));
 #pragma unroll
                     for (int t = 0; t < 2; t++) {
-                        float *d = NV ? acc[t][n] : part[t][n];
+                        float *d = part[t][n];
                         mma_f16(d, h[2 * t][0], h[2 * t + 1][0], h[2 * t][1], h[2 * t + 1][1], bx[0], bx[1]);
                         mma_f16(d, h[2 * t][2], h[2 * t + 1][2], h[2 * t][3], h[2 * t + 1][3], bx[2], bx[3]);
                     }
                 }
             }
-            if (!NV) {
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    const float f0 = exp2i((int)ref[2 * t] - 127), f1 = exp2i((int)ref[2 * t + 1] - 127);
+            for (int t = 0; t < 2; t++) {
+                const float f0 = NV ? 1.0f : exp2i((int)ref[2 * t] - 127), f1 = NV ? 1.0f : exp2i((int)ref[2 * t + 1] - 127);
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);
-                        acc[t][n][1] = __fmaf_rn(part[t][n][1], f0, acc[t][n][1]);
-                        acc[t][n][2] = __fmaf_rn(part[t][n][2], f1, acc[t][n][2]);
-                        acc[t][n][3] = __fmaf_rn(part[t][n][3], f1, acc[t][n][3]);
-                    }
+                for (int n = 0; n < NT; n++) {
+                    acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);
+                    acc[t][n][1] = __fmaf_rn(part[t][n][1], f0, acc[t][n][1]);
+                    acc[t][n][2] = __fmaf_rn(part[t][n][2], f1, acc[t][n][2]);
+                    acc[t][n][3] = __fmaf_rn(part[t][n][3], f1, acc[t][n][3]);
                 }
             }
         }
     }
 
     // ---- sums: warps along K, hi and lo columns, then the cluster ----
+    cp_async_wait<0>();
     __syncthreads();
     float *red = reinterpret_cast<float *>(smem);            // [WK][cols][ROWS]
     float *sum = red + WK * a.cols * ROWS;                   // [M][ROWS]
@@ -290,34 +295,34 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
         }
         sum[i] = __fmul_rn(s, x_up[m]);
     }
-    cluster_sync();
     const uint32_t cl = (uint32_t)a.cluster;
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
     const float gw = NV ? *a.gw : 0.00390625f;  // e8m0_rel's 2^8
     for (int i = threadIdx.x * cl + rank; i < a.M * ROWS; i += kThreads * cl) {
         const int m = i / ROWS, row = i % ROWS;
         const int64_t n = atom * 128 + (row / (8 * WR)) * 32 + (tile % (4 / WR)) * (8 * WR) + row % (8 * WR);
-        float s = 0.0f;
-        for (uint32_t r = 0; r < cl; r++) s = __fadd_rn(s, ld_shared_cluster_f32(mapa_shared(smem_u32(sum + i), r)));
-        s = __fmul_rn(s, gw);
+        float t = 0.0f;
+        for (uint32_t r = 0; r < cl; r++) t = __fadd_rn(t, ld_shared_cluster_f32(mapa_shared(smem_u32(sum + i), r)));
+        t = __fmul_rn(t, gw);
         if (n < a.N) {
             if (BF16OUT)
-                static_cast<__nv_bfloat16 *>(a.out)[m * a.ldc + n] = __float2bfloat16_rn(s);
+                static_cast<__nv_bfloat16 *>(a.out)[m * a.ldc + n] = __float2bfloat16_rn(t);
             else
-                static_cast<float *>(a.out)[m * a.ldc + n] = s;
+                static_cast<float *>(a.out)[m * a.ldc + n] = t;
         }
     }
-    cluster_sync();  // no CTA leaves while another reads its sums
+    if (cl > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 struct Plan {
     int wr, cluster, slice, stage;
 };
 
-// Cuts N into tiles of 32 * wr rows and K into cluster slices: the cheapest
-// by rounds of resident CTAs, each a fixed start plus its warps' steps.
+// Cuts N into tiles of 32 * wr rows and K into cluster slices.
 static Plan plan(int64_t N, int64_t K, int cols, int sms)
 {
-    const int64_t chunks = std::max<int64_t>((K + 127) / 128, 1), atoms = (N + 127) / 128;
+    const int64_t chunks = (K + 127) / 128, atoms = (N + 127) / 128;
     Plan best = {};
     double least = 0.0;
     for (int wr = 4; wr >= 1; wr /= 2) {
@@ -327,9 +332,9 @@ static Plan plan(int64_t N, int64_t K, int cols, int sms)
             if ((chunks + slice - 1) / slice != cl) continue;  // every CTA has work
             const int64_t steps = (slice + wk - 1) / wk;
             const int64_t ctas = atoms * (4 / wr) * cl;
-            const int64_t rounds = (ctas + 3 * sms - 1) / (3 * sms);
-            const double full = (double)std::min<int64_t>(ctas, 3 * (int64_t)sms) / (3.0 * sms);
-            const double cost = rounds * (2.5 + 0.0005 * cols * slice + (0.4 + 0.85 * full) * steps);
+            const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
+            const double full = (double)std::min<int64_t>(ctas, 2 * (int64_t)sms) / (2.0 * sms);
+            const double cost = rounds * (2.5 + 0.005 * cols * slice + (0.3 + 0.3 * full) * steps);
             if (best.wr == 0 || cost < least) {
                 least = cost;
                 int64_t stage = (kXBytes / cols - 64) / 256 / wk * wk;
@@ -347,8 +352,9 @@ static cudaError_t launch_t(const Args &a, const Plan &p, cudaStream_t st)
     auto kern = w4a16_kernel<FMT, WR, NT, BF16OUT>;
     const size_t x = (size_t)a.cols * (a.stage * 256 + 64);
     const size_t red = (size_t)(8 / WR) * a.cols * 32 * WR * 4 + (size_t)a.M * 32 * WR * 4;
-    const size_t smem = std::max(x, red);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = std::max(kRing + x, red);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kMaxSmem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.N + 127) / 128 * (4 / WR) * p.cluster));
