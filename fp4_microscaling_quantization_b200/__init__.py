@@ -16,7 +16,7 @@ from ._lib import (FP4_MX_SCALE_CEIL, FP4_MX_SCALE_FLOOR, FP4_MXFP4, FP4_MXFP4_1
 
 __all__ = [
     "quantize", "dequantize", "gemm", "gemm_quantized", "linear", "linear_residual", "linear_workspace_size",
-    "quantize_sizes", "linear_w4a16", "KVCache", "kv_cache_sizes", "kv_append", "kv_gather", "paged_attention",
+    "quantize_sizes", "linear_w4a16", "linear_w4a16_workspace_size", "KVCache", "kv_cache_sizes", "kv_append", "kv_gather", "paged_attention",
     "paged_attention_workspace_size",
     "gemm_workspace_size", "check_device_status", "kernel_launches",
     "FP4_MXFP4", "FP4_NVFP4", "FP4_MXFP4_16", "FP4_ROUND_EVEN", "FP4_ROUND_AWAY", "FP4_MX_SCALE_CEIL",
@@ -47,8 +47,10 @@ def _run(name: str, device, *args) -> None:
     stream the call is given."""
     import torch
 
-    if torch.cuda.current_device() == device.index:
-        _lib.check(name, getattr(_lib.lib(), name)(*args))
+    if torch._C._cuda_getDevice() == device.index:  # (the tensors' being on the GPU has initialised CUDA)
+        code = getattr(_lib.lib(), name)(*args)
+        if code:
+            _lib.check(name, code)
         return
     with torch.cuda.device(device):
         _lib.check(name, getattr(_lib.lib(), name)(*args))
@@ -393,7 +395,23 @@ def linear_residual(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF1
     return out
 
 
-def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, out=None,
+def linear_w4a16_workspace_size(M: int, N: int, K: int, fmt) -> int:
+    """Scratch bytes of a linear_w4a16 call of these sizes on the current device."""
+    b = ctypes.c_size_t()
+    _lib.check("fp4_linear_w4a16_workspace_size",
+               _lib.lib().fp4_linear_w4a16_workspace_size(M, N, K, _fmt(fmt), ctypes.byref(b)))
+    return b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _w4a16_scratch(device: int, *sizes) -> int:
+    import torch
+
+    with torch.cuda.device(device):
+        return linear_w4a16_workspace_size(*sizes)
+
+
+def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, out=None, workspace=None,
                  weights_static: bool = False):
     """The weight-only decode linear (M <= 16, see fp4_linear_w4a16): C = x W^T
     with FP4 weights w = (Wq, Ws, gW) as for :func:`linear` and bf16
@@ -413,10 +431,16 @@ def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, 
         out = torch.empty((M, N), dtype=dt, device=x.device)
     else:
         _out2d(out, M, N, dt, "out", x.device)
+    need = _w4a16_scratch(x.device.index, M, N, K, fmt)
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        _dev(workspace, "workspace", x.device, torch.uint8)
     _run("fp4_linear_w4a16", x.device,
          x.data_ptr(), M, K, x.stride(0) if M > 1 else (K + 7) // 8 * 8, fmt, int(hadamard_k),
          _opts(0, 0, 0, 0, int(bool(weights_static))),
          Wq.data_ptr(), Ws.data_ptr(), gW.data_ptr(), N, int(out_dtype), out.data_ptr(), out.stride(0) if M > 1 else N,
+         workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0,
          _stream_handle(torch, x.device))
     return out
 
@@ -502,14 +526,15 @@ def kv_append(cache: KVCache, k, v, slots, round: int = FP4_ROUND_EVEN, mx_scale
     import torch
 
     tokens = _slots(slots, cache.device)
-    for name, t in (("k", k), ("v", v)):
+    shape, ks, vs = (tokens, cache.kv_heads, cache.head_dim), k.stride(), v.stride()
+    for name, t, st in (("k", k, ks), ("v", v, vs)):
         _dev(t, name, cache.device, torch.bfloat16, contiguous=False)
-        if tuple(t.shape) != (tokens, cache.kv_heads, cache.head_dim) or (t.numel() and t.stride(2) != 1):
-            raise ValueError(f"{name} must be ({tokens}, {cache.kv_heads}, {cache.head_dim}), contiguous along its last axis")
+        if t.shape != shape or (tokens and st[2] != 1):
+            raise ValueError(f"{name} must be {shape}, contiguous along its last axis")
     many, heads = tokens > 1, cache.kv_heads > 1
     _run("fp4_kv_append", cache.device,
-         cache._p, k.data_ptr(), k.stride(0) if many else 0, k.stride(1) if heads else 0, v.data_ptr(),
-         v.stride(0) if many else 0, v.stride(1) if heads else 0, slots.data_ptr(), tokens,
+         cache._p, k.data_ptr(), ks[0] if many else 0, ks[1] if heads else 0, v.data_ptr(), vs[0] if many else 0,
+         vs[1] if heads else 0, slots.data_ptr(), tokens,
          _opts(int(round), int(mx_scale_rule), 1, 0, 0), _stream_handle(torch, cache.device))
 
 
@@ -523,8 +548,7 @@ def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if out is None:
-        k = torch.empty(shape, dtype=dt, device=cache.device)
-        v = torch.empty(shape, dtype=dt, device=cache.device)
+        k, v = torch.empty((2, *shape), dtype=dt, device=cache.device).unbind(0)
     else:
         k, v = out
         for name, t in (("k", k), ("v", v)):
@@ -568,7 +592,8 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
 
     dev = cache.device
     _dev(q, "q", dev, torch.bfloat16, contiguous=False)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or (q.numel() and q.stride(2) != 1):
+    qs = q.stride()
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or (q.numel() and qs[2] != 1):
         raise ValueError(f"q must be (batch, q_heads, {cache.head_dim}), contiguous along its last axis")
     batch, heads = q.shape[0], q.shape[1]
     _dev(page_table, "page_table", dev, torch.int32, contiguous=False)
@@ -592,7 +617,7 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
     if workspace is not None:
         _dev(workspace, "workspace", dev, torch.uint8)
     _run("fp4_paged_attention", dev,
-         cache._p, q.data_ptr(), batch, heads, q.stride(0) if batch > 1 else 0, q.stride(1) if heads > 1 else 0,
+         cache._p, q.data_ptr(), batch, heads, qs[0] if batch > 1 else 0, qs[1] if heads > 1 else 0,
          page_table.data_ptr(), page_table.stride(0) if batch > 1 else cols, cols, seq_lens.data_ptr(), int(max_seq_len),
          cache.head_dim ** -0.5 if scale is None else float(scale), int(window), int(out_dtype), out.data_ptr(),
          lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,

@@ -57,7 +57,9 @@ SIGNATURES = {
     "fp4_paged_attention_workspace_size": (_int, [_i64, _int, _int, _int, _i64, _i64, ctypes.POINTER(_sz)]),
     "fp4_paged_attention": (_int, [_vp, _vp, _i64, _int, _i64, _i64, _vp, _i64, _i64, _vp, _i64, ctypes.c_float, _i64,
                                    _int, _vp, _vp, _vp, _sz, _vp]),
-    "fp4_linear_w4a16": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64, _vp]),
+    "fp4_linear_w4a16_workspace_size": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_sz)]),
+    "fp4_linear_w4a16": (_int, [_vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, _i64, _int, _vp, _i64, _vp, _sz,
+                                _vp]),
     "fp4_kernel_launches": (ctypes.c_uint64, []),
     "fp4_test_inject_stall": (_int, [_int, ctypes.c_uint64]),
 }

@@ -760,7 +760,7 @@ struct Plan {
 // (64 sequences of 1 to 8192 tokens: 4096 a chunk 98 us, 2048 88, 1024 88).
 // (One exact round for the long sequence: 75 us; 1.7 rounds of
 // half the chunk 79 us, 1.2 rounds 87 us.)
-static Plan plan(int64_t batch, int kv_heads, int head_tiles, int dim, int64_t tokens, int sms)
+static Plan search(int64_t batch, int kv_heads, int head_tiles, int dim, int64_t tokens, int sms)
 {
     const int64_t rows = batch * kv_heads * head_tiles, slots = (int64_t)sms * (dim == 256 ? 2 : 4);
     const int64_t step = NW * (dim == 64 ? 64 : dim == 128 ? 32 : 16);
@@ -784,6 +784,23 @@ static Plan plan(int64_t batch, int kv_heads, int head_tiles, int dim, int64_t t
     for (int64_t r = 1; r <= 2; r++)  // whole rounds
         if (r * slots / rows >= 1 && r * slots / rows <= kMaxChunks) consider(r * slots / rows);
     return best;
+}
+
+// The last search of this thread is kept: a decode loop asks for the same sizes
+// again and again, and a search takes longer than a launch.
+static Plan plan(int64_t batch, int kv_heads, int head_tiles, int dim, int64_t tokens, int sms)
+{
+    struct Last {
+        int64_t key[6];
+        Plan p;
+    };
+    static thread_local Last last = {{-1, -1, -1, -1, -1, -1}, {}};
+    const int64_t key[6] = {batch, kv_heads, head_tiles, dim, tokens, sms};
+    if (!std::equal(key, key + 6, last.key)) {
+        last.p = search(batch, kv_heads, head_tiles, dim, tokens, sms);
+        std::copy(key, key + 6, last.key);
+    }
+    return last.p;
 }
 
 // Tokens that a sequence's chunks have to cover: its live range from the last

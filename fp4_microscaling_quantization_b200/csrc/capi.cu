@@ -41,9 +41,9 @@ cudaError_t launch_linear_fused(const uint16_t *x, int64_t ldx, int64_t M, int64
                                 bool w_before_wait, bool residual, bool *taken);
 cudaError_t launch_kv_append(const KvView &c, int dim, int fmt, int hk, float ck, const uint16_t *k, int64_t k_tok,
                              int64_t k_head, const uint16_t *v, int64_t v_tok, int64_t v_head, const int64_t *slots,
-                             int64_t tokens, int round_away, int mx_floor, cudaStream_t st, bool *too_many);
+                             int64_t tokens, int round_away, int mx_floor, int sms, cudaStream_t st, bool *too_many);
 cudaError_t launch_kv_gather(const KvView &c, int dim, int fmt, int hk, float ck, const int64_t *slots, int64_t tokens,
-                             int bf16out, void *k, void *v, cudaStream_t st, bool *too_many);
+                             int bf16out, void *k, void *v, int sms, cudaStream_t st, bool *too_many);
 size_t paged_attention_workspace_bytes(int64_t batch, int q_heads, int kv_heads, int dim, int64_t max_len, int64_t window,
                                        int sms);
 cudaError_t launch_paged_attention(const KvView &c, int dim, int fmt, int hk, float ck, const uint16_t *q, int64_t batch,
@@ -52,7 +52,8 @@ cudaError_t launch_paged_attention(const KvView &c, int dim, int fmt, int hk, fl
                                    int bf16out, void *out, float *lse, void *ws, int sms, cudaStream_t st);
 cudaError_t launch_linear_w4a16(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, int fmt, int hk, float ck,
                                 const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N, int bf16out, void *C,
-                                int64_t ldc, int w_early, int sms, cudaStream_t st);
+                                int64_t ldc, int w_early, void *ws, int sms, cudaStream_t st);
+size_t linear_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int cols, bool rotated, int sms);
 cudaError_t read_and_clear_device_errors(cudaStream_t st, unsigned int *err);
 static std::atomic<uint64_t> g_launches{0};
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
@@ -521,7 +522,7 @@ fp4_status fp4_kv_append(const fp4_kv_cache *cache, const void *k, int64_t k_tok
         c, cache->head_dim, cache->fmt, cache->hadamard_k, hadamard_constant(cache->hadamard_k),
         static_cast<const uint16_t *>(k), k_token_stride, k_head_stride, static_cast<const uint16_t *>(v), v_token_stride,
         v_head_stride, slots, tokens, o.round == FP4_ROUND_AWAY, o.mx_scale_rule == FP4_MX_SCALE_FLOOR,
-        static_cast<cudaStream_t>(stream), &too_many);
+        sm_count(), static_cast<cudaStream_t>(stream), &too_many);
     if (too_many) return FP4_ERR_UNSUPPORTED;
     return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
@@ -540,7 +541,7 @@ fp4_status fp4_kv_gather(const fp4_kv_cache *cache, const int64_t *slots, int64_
     bool too_many = false;
     const cudaError_t e = fp4::launch_kv_gather(c, cache->head_dim, cache->fmt, cache->hadamard_k,
                                                 hadamard_constant(cache->hadamard_k), slots, tokens,
-                                                out_dtype == FP4_OUT_BF16, k_out, v_out,
+                                                out_dtype == FP4_OUT_BF16, k_out, v_out, sm_count(),
                                                 static_cast<cudaStream_t>(stream), &too_many);
     if (too_many) return FP4_ERR_UNSUPPORTED;
     return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
@@ -589,9 +590,24 @@ fp4_status fp4_paged_attention(const fp4_kv_cache *cache, const void *q, int64_t
     return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
+fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int fmt, size_t *bytes)
+{
+    if (M < 0 || N < 0 || K < 0 || !bytes) return FP4_ERR_INVALID_ARG;
+    if (!valid_gemm_fmt(fmt)) return FP4_ERR_UNSUPPORTED;
+    if (M > 16 || N > (1 << 30) || K > (1 << 30)) return FP4_ERR_UNSUPPORTED;  // as fp4_linear_w4a16
+    const int sms = sm_count();
+    *bytes = 0;  // the most that any rotation and output type takes
+    for (int rot = 0; rot < 2; rot++)
+        for (int two = 0; two <= rot; two++) {
+            const size_t need = fp4::linear_w4a16_workspace_bytes(M, N, K, (int)(two ? 2 * M : M), rot != 0, sms);
+            if (need > *bytes) *bytes = need;
+        }
+    return FP4_OK;
+}
+
 fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
                             const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,
-                            int out_dtype, void *C, int64_t ldc, void *stream)
+                            int out_dtype, void *C, int64_t ldc, void *workspace, size_t ws_bytes, void *stream)
 {
     const int w_static = opts ? opts->weights_static : 0;
     if (M < 0 || N < 0 || K < 0 || ld_x < K || ldc < N) return FP4_ERR_INVALID_ARG;
@@ -607,9 +623,13 @@ fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, i
     if (fmt == FP4_NVFP4 && !gW) return FP4_ERR_INVALID_ARG;
     if (!aligned(x, 16) || (ld_x % 8) || !aligned(Wq, 16) || !aligned(Ws, 16) || !aligned(C, 16) || !aligned(gW, 4))
         return FP4_ERR_ALIGNMENT;
+    const int sms = sm_count(), cols = (int)(hadamard_k && out_dtype == FP4_OUT_F32 ? 2 * M : M);
+    const size_t need = fp4::linear_w4a16_workspace_bytes(M, N, K, cols, hadamard_k != 0, sms);
+    if (need > 0 && (!workspace || ws_bytes < need)) return FP4_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, 256)) return FP4_ERR_ALIGNMENT;
     const cudaError_t e = fp4::launch_linear_w4a16(
         static_cast<const uint16_t *>(x), ld_x, M, K, fmt, hadamard_k, hadamard_constant(hadamard_k), Wq, Ws, gW, N,
-        out_dtype == FP4_OUT_BF16, C, ldc, w_static, sm_count(), static_cast<cudaStream_t>(stream));
+        out_dtype == FP4_OUT_BF16, C, ldc, w_static, workspace, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 

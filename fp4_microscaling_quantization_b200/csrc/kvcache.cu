@@ -9,11 +9,16 @@
 // the cache, not to one call's tokens.
 //
 // Work decomposition: one thread owns one 32-element unit of a head row
-// (64 bytes of bf16, 16 bytes of nibbles, 1 or 2 scale bytes).  A warp owns
-// 32 / (dim / 32) consecutive tokens of one head of K or of V: with
-// consecutive slots its nibbles are 512 contiguous bytes of a page, and its
-// bf16 rows are whole 2 * dim byte segments.  Bound: HBM for prompts, the
-// launch and two dependent loads (slot, then data) for a decode step.
+// (64 bytes of bf16, 16 bytes of nibbles, 1 or 2 scale bytes) of K and the
+// same of V, both loads ahead of the first use; calls that do not fill the GPU
+// give K and V to different warps (61 tokens: append and gather 4.0 us, by one
+// warp 5.1).  A warp owns 32 / (dim / 32)
+// consecutive tokens of one head: with consecutive slots its nibbles are 512
+// contiguous bytes of a page, and its bf16 rows are whole 2 * dim byte
+// segments, read and written 32 bytes a lane.  Bound: HBM for prompts, at 64
+// and 128 the rotation's issue slots; the launch and two dependent loads
+// (slot, then data) for a decode step.
+#include "frag.cuh"
 #include "kv.cuh"
 #include "sm100.cuh"
 
@@ -29,26 +34,32 @@ struct KvAppendArgs {
     int upr_shift;  // log2 of the units in a head row (1, 2, 3)
     float ck;
     int round_away, mx_floor;
-    uint32_t warps;  // 2 * heads * token groups
+    int wide;       // rows are 32-byte aligned: 32-byte loads
+    uint32_t warps;  // heads * token groups (of a grid row)
     FastDiv heads_div;
 };
 
-// The token, head and tensor (0 = K, 1 = V) of a warp, and its lane's unit.
+// The head of a warp, its lane's token and unit of the head row.
 struct KvWork {
     int64_t token;
-    int head, kv, unit;
+    int head, unit;
 };
 
 FP4_DEV KvWork kv_work(uint32_t warp, int lane, int upr_shift, const FastDiv &heads_div)
 {
     KvWork w;
-    w.kv = warp & 1;
-    const uint32_t th = warp >> 1;
-    const uint32_t group = fastdiv(th, heads_div);
-    w.head = (int)(th - group * heads_div.d);
+    const uint32_t group = fastdiv(warp, heads_div);
+    w.head = (int)(warp - group * heads_div.d);
     w.unit = lane & ((1 << upr_shift) - 1);
     w.token = (int64_t)group * (32 >> upr_shift) + (lane >> upr_shift);
     return w;
+}
+
+FP4_DEV void ldg_v8(const void *p, uint4 &a, uint4 &b)
+{
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
 }
 
 template <int FMT, int HK>
@@ -60,33 +71,47 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a)
     if (warp >= a.warps) return;
     const int lane = threadIdx.x & 31;
     const KvWork w = kv_work(warp, lane, a.upr_shift, a.heads_div);
+    const int only = gridDim.y == 2 ? (int)blockIdx.y : -1;  // K or V alone
     const int64_t slot = w.token < a.tokens ? __ldg(a.slots + w.token) : -1;
     const bool live = slot >= 0 && slot < a.num_slots;  // others are dropped
-    float sg = 1.0f, six_sg = 6.0f;
-    if (FMT == FP4_NVFP4) {
-        sg = __ldg(w.kv ? a.c.gv : a.c.gk);
-        six_sg = __fmul_rn(6.0f, sg);
-    }
-    uint4 raw[4] = {};
+    uint4 raw[2][4] = {};
     if (live) {
-        const uint16_t *row = w.kv ? a.v + w.token * a.v_tok + w.head * a.v_head : a.k + w.token * a.k_tok + w.head * a.k_head;
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + w.unit * 32);
 #pragma unroll
-        for (int i = 0; i < 4; i++) raw[i] = __ldg(p + i);
+        for (int i = 0; i < 2; i++) {
+            if (i + only == 1) continue;
+            const uint16_t *row = i ? a.v + w.token * a.v_tok + w.head * a.v_head : a.k + w.token * a.k_tok + w.head * a.k_head;
+            const uint4 *p = reinterpret_cast<const uint4 *>(row + w.unit * 32);
+            if (a.wide) {
+                ldg_v8(p, raw[i][0], raw[i][1]);
+                ldg_v8(p + 2, raw[i][2], raw[i][3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) raw[i][e] = __ldg(p + e);
+            }
+        }
     }
-    float v[32];
-    unpack_unit(raw, v);
-    if (HK) fwht_unit<HK>(v, a.ck, lane);  // every lane: chunks of 64 and 128 exchange values
-    uint4 out;
-    const uint32_t sb = encode_unit<FMT>(v, sg, six_sg, a.round_away, a.mx_floor, out);
-    if (!live) return;
-    const int64_t unit = (kv_row(slot, w.head, a.c) << a.upr_shift) + w.unit;
-    reinterpret_cast<uint4 *>(w.kv ? a.c.vq : a.c.kq)[unit] = out;
-    uint8_t *s = w.kv ? a.c.vs : a.c.ks;
-    if (FMT == FP4_MXFP4)
-        s[unit] = (uint8_t)sb;
-    else
-        reinterpret_cast<uint16_t *>(s)[unit] = (uint16_t)sb;
+    const int64_t unit = live ? (kv_row(slot, w.head, a.c) << a.upr_shift) + w.unit : 0;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        if (i + only == 1) continue;
+        float sg = 1.0f, six_sg = 6.0f;
+        if (FMT == FP4_NVFP4) {
+            sg = __ldg(i ? a.c.gv : a.c.gk);
+            six_sg = __fmul_rn(6.0f, sg);
+        }
+        float v[32];
+        unpack_unit(raw[i], v);
+        if (HK) fwht_unit<HK>(v, a.ck, lane);  // every lane: chunks of 64 and 128 exchange values
+        uint4 out;
+        const uint32_t sb = encode_unit<FMT>(v, sg, six_sg, a.round_away, a.mx_floor, out);
+        if (!live) continue;
+        reinterpret_cast<uint4 *>(i ? a.c.vq : a.c.kq)[unit] = out;
+        uint8_t *s = i ? a.c.vs : a.c.ks;
+        if (FMT == FP4_MXFP4)
+            s[unit] = (uint8_t)sb;
+        else
+            reinterpret_cast<uint16_t *>(s)[unit] = (uint16_t)sb;
+    }
 }
 
 struct KvGatherArgs {
@@ -111,50 +136,63 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a)
     const int lane = threadIdx.x & 31;
     const KvWork w = kv_work(warp, lane, a.upr_shift, a.heads_div);
     const bool live = w.token < a.tokens;
+    const int only = gridDim.y == 2 ? (int)blockIdx.y : -1;  // K or V alone
     const int64_t slot = live ? __ldg(a.slots + w.token) : -1;
-    const float sg = (FMT == FP4_NVFP4) ? __ldg(w.kv ? a.c.gv : a.c.gk) : 1.0f;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    uint32_t sb = 0;
+    uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    uint32_t sb[2] = {0, 0};
     const bool held = slot >= 0 && slot < a.num_slots;  // others read as zeros
     if (held) {
         const int64_t unit = (kv_row(slot, w.head, a.c) << a.upr_shift) + w.unit;
-        raw = __ldg(reinterpret_cast<const uint4 *>(w.kv ? a.c.vq : a.c.kq) + unit);
-        const uint8_t *s = w.kv ? a.c.vs : a.c.ks;
-        sb = (FMT == FP4_MXFP4) ? (uint32_t)__ldg(s + unit) : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s) + unit);
-    }
-    const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
-    float d0, d1, v[32];
-    unit_decode_factors<FMT>(sb, sg, d0, d1);
-    if (!held) d0 = d1 = 0.0f;  // a tensor scale that is not finite reaches no zero
 #pragma unroll
-    for (int c = 0; c < 4; c++) {
-#pragma unroll
-        for (int b = 0; b < 4; b++) {
-            float lo, hi;
-            e2m1x2_to_f32((words[c] >> (8 * b)) & 0xFF, lo, hi);
-            v[8 * c + 2 * b] = __fmul_rn(c < 2 ? d0 : d1, lo);
-            v[8 * c + 2 * b + 1] = __fmul_rn(c < 2 ? d0 : d1, hi);
+        for (int i = 0; i < 2; i++) {
+            if (i + only == 1) continue;
+            raw[i] = __ldg(reinterpret_cast<const uint4 *>(i ? a.c.vq : a.c.kq) + unit);
+            const uint8_t *s = i ? a.c.vs : a.c.ks;
+            sb[i] = (FMT == FP4_MXFP4) ? (uint32_t)__ldg(s + unit) : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s) + unit);
         }
     }
-    if (HK) fwht_unit<HK>(v, a.ck, lane);
-    if (!live) return;
-    // 32-byte stores: whole sectors from each lane, so no staging for the
-    // write side is needed
     const int64_t unit = ((w.token * a.c.heads + w.head) << a.upr_shift) + w.unit;
-    if (BF16OUT) {
-        uint8_t *p = static_cast<uint8_t *>(w.kv ? a.v : a.k) + unit * 64;
-        uint32_t h[16];
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            h[i] = *reinterpret_cast<const uint32_t *>(&t);
+    for (int i = 0; i < 2; i++) {
+        if (i + only == 1) continue;
+        const float sg = (FMT == FP4_NVFP4) ? __ldg(i ? a.c.gv : a.c.gk) : 1.0f;
+        const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float d0, d1, v[32];
+        unit_decode_factors<FMT>(sb[i], sg, d0, d1);
+        if (!held) d0 = d1 = 0.0f;  // a tensor scale that is not finite reaches no zero
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+            uint32_t h[4];
+            e2m1x8_to_f16(words[c], h);
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&h[b]));
+                v[8 * c + 2 * b] = t.x;
+                v[8 * c + 2 * b + 1] = t.y;
+            }
         }
-        st_global_v8(p, h);
-        st_global_v8(p + 32, h + 8);
-    } else {
-        uint8_t *p = static_cast<uint8_t *>(w.kv ? a.v : a.k) + unit * 128;
+        // RN(d q): the scale times an exact value, each rounded on its own
 #pragma unroll
-        for (int i = 0; i < 4; i++) st_global_v8(p + 32 * i, reinterpret_cast<const uint32_t *>(v) + 8 * i);
+        for (int e = 0; e < 32; e++) v[e] = __fmul_rn(e < 16 ? d0 : d1, v[e]);
+        if (HK) fwht_unit<HK>(v, a.ck, lane);
+        if (!live) continue;
+        // 32-byte stores: whole sectors from each lane, so no staging for the
+        // write side is needed
+        if (BF16OUT) {
+            uint8_t *p = static_cast<uint8_t *>(i ? a.v : a.k) + unit * 64;
+            uint32_t h[16];
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                h[e] = *reinterpret_cast<const uint32_t *>(&t);
+            }
+            st_global_v8(p, h);
+            st_global_v8(p + 32, h + 8);
+        } else {
+            uint8_t *p = static_cast<uint8_t *>(i ? a.v : a.k) + unit * 128;
+#pragma unroll
+            for (int e = 0; e < 4; e++) st_global_v8(p + 32 * e, reinterpret_cast<const uint32_t *>(v) + 8 * e);
+        }
     }
 }
 
@@ -188,15 +226,18 @@ static void (*gather_for(int hk))(KvGatherArgs)
 static uint32_t kv_warps(int64_t tokens, int heads, int upr_shift)
 {
     const int64_t groups = (tokens + (32 >> upr_shift) - 1) / (32 >> upr_shift);
-    if (groups > (int64_t(1) << 31) / (2 * (int64_t)heads)) return 0;
-    return (uint32_t)(2 * heads * groups);
+    if (groups > (int64_t(1) << 31) / heads) return 0;
+    return (uint32_t)(heads * groups);
 }
+
+// Eight warps to a CTA; a second row of CTAs for V up to one round of 24 warps per SM.
+static dim3 kv_grid(uint32_t warps, int sms) { return dim3((warps + 7) / 8, warps <= (uint32_t)sms * 12 ? 2 : 1); }
 
 static int upr_shift_of(int dim) { return dim == 64 ? 1 : dim == 128 ? 2 : 3; }
 
 cudaError_t launch_kv_append(const KvView &c, int dim, int fmt, int hk, float ck, const uint16_t *k, int64_t k_tok,
                              int64_t k_head, const uint16_t *v, int64_t v_tok, int64_t v_head, const int64_t *slots,
-                             int64_t tokens, int round_away, int mx_floor, cudaStream_t st, bool *too_many)
+                             int64_t tokens, int round_away, int mx_floor, int sms, cudaStream_t st, bool *too_many)
 {
     KvAppendArgs a = {};
     a.c = c;
@@ -213,16 +254,17 @@ cudaError_t launch_kv_append(const KvView &c, int dim, int fmt, int hk, float ck
     a.ck = ck;
     a.round_away = round_away;
     a.mx_floor = mx_floor;
+    a.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0) && (k_tok | k_head | v_tok | v_head) % 16 == 0;
     a.warps = kv_warps(tokens, c.heads, a.upr_shift);
     a.heads_div = make_fastdiv((uint32_t)c.heads);
     *too_many = a.warps == 0;
     if (*too_many) return cudaSuccess;
     auto kern = fmt == FP4_MXFP4 ? append_for<FP4_MXFP4>(hk) : fmt == FP4_NVFP4 ? append_for<FP4_NVFP4>(hk) : append_for<FP4_MXFP4_16>(hk);
-    return launch_k(kern, dim3((a.warps + 7) / 8), dim3(256), 0, st, true, a);
+    return launch_k(kern, kv_grid(a.warps, sms), dim3(256), 0, st, true, a);
 }
 
 cudaError_t launch_kv_gather(const KvView &c, int dim, int fmt, int hk, float ck, const int64_t *slots, int64_t tokens,
-                             int bf16out, void *k, void *v, cudaStream_t st, bool *too_many)
+                             int bf16out, void *k, void *v, int sms, cudaStream_t st, bool *too_many)
 {
     KvGatherArgs a = {};
     a.c = c;
@@ -242,7 +284,7 @@ cudaError_t launch_kv_gather(const KvView &c, int dim, int fmt, int hk, float ck
         kern = fmt == FP4_MXFP4 ? gather_for<FP4_MXFP4, 1>(hk) : fmt == FP4_NVFP4 ? gather_for<FP4_NVFP4, 1>(hk) : gather_for<FP4_MXFP4_16, 1>(hk);
     else
         kern = fmt == FP4_MXFP4 ? gather_for<FP4_MXFP4, 0>(hk) : fmt == FP4_NVFP4 ? gather_for<FP4_NVFP4, 0>(hk) : gather_for<FP4_MXFP4_16, 0>(hk);
-    return launch_k(kern, dim3((a.warps + 7) / 8), dim3(256), 0, st, true, a);
+    return launch_k(kern, kv_grid(a.warps, sms), dim3(256), 0, st, true, a);
 }
 
 }  // namespace fp4

@@ -28,6 +28,8 @@
 // each), 8 / WR along K; a cluster of up to 8 CTAs splits K further and joins
 // its sums over distributed shared memory in a fixed order.  One launch, no
 // workspace, results repeat bit for bit.
+#include <math.h>
+
 #include <algorithm>
 
 #include "frag.cuh"
@@ -60,6 +62,93 @@ struct Args {
     int cluster;          // CTAs that share a tile
     int w_early;          // W may be read before the grid-dependency wait
 };
+
+// A lane's part of a step of W: 32 elements and a scale word of 4 rows.
+struct Piece {
+    uint32_t w[4][4], s[4];
+};
+
+FP4_DEV void take(uint32_t at, Piece &p)
+{
+#pragma unroll
+    for (int j = 0; j < 4; j++) lds(at + j * 512, p.w[j], 4);
+    lds(at + 2048, p.s, 4);
+}
+
+// One warp's step: 32 rows of W (a lane's part p) times 128 elements of the
+// columns of x at `xb` (this lane's pieces, `pitch` bytes a column).
+// Columns from `cols` on count as zeros (8 * NT: all are there).
+template <int FMT, int NT, int BF16OUT>
+FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols, int g, int c, float (&acc)[2][NT][4])
+{
+    constexpr bool NV = FMT == FP4_NVFP4;
+    // The step's own sums, added with a rounding to nearest, which the product's
+    // accumulation of many steps would not give.  Not needed for NVFP4 with
+    // bf16 output: what it loses (1e-6 at K = 8192) is far below 2^-9.
+    constexpr bool PART = !NV || !BF16OUT;
+    uint32_t sc[4][2], ref[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        if (FMT == FP4_MXFP4) {
+            ref[j] = max_byte(p.s[j]);
+            sc[j][0] = sc[j][1] = e8m0_rel((p.s[j] >> (8 * c)) & 0xFF, ref[j]);
+        } else {
+            const uint32_t two = (p.s[j] >> (16 * (c & 1))) & 0xFFFF;
+            if (NV) {
+                const uint32_t f = e4m3x2_to_f16x2(two);
+                sc[j][0] = __byte_perm(f, 0, 0x1010);
+                sc[j][1] = __byte_perm(f, 0, 0x3232);
+            } else {
+                ref[j] = max_byte(p.s[j]);
+                ref[j] = max(ref[j], __shfl_xor_sync(0xFFFFFFFFu, ref[j], 2));  // the step's other scale word
+                sc[j][0] = e8m0_rel(two & 0xFF, ref[j]);
+                sc[j][1] = e8m0_rel(two >> 8, ref[j]);
+            }
+        }
+    }
+    float part[2][NT][4];
+    if (PART) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int n = 0; n < NT; n++) part[t][n][0] = part[t][n][1] = part[t][n][2] = part[t][n][3] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t h[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            e2m1x8_to_f16(p.w[j][i], h[j]);
+#pragma unroll
+            for (int e = 0; e < 4; e++) h[j][e] = mul_f16x2(h[j][e], sc[j][i >> 1]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            uint32_t bx[4] = {0, 0, 0, 0};
+            if (8 * n + g < cols)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(bx[0]), "=r"(bx[1]), "=r"(bx[2]), "=r"(bx[3]) : "r"(xb + (8 * n + g) * pitch + i * 64));
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                float *d = PART ? part[t][n] : acc[t][n];
+                mma_f16(d, h[2 * t][0], h[2 * t + 1][0], h[2 * t][1], h[2 * t + 1][1], bx[0], bx[1]);
+                mma_f16(d, h[2 * t][2], h[2 * t + 1][2], h[2 * t][3], h[2 * t + 1][3], bx[2], bx[3]);
+            }
+        }
+    }
+    if (PART) {
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            const float f0 = NV ? 1.0f : exp2i((int)ref[2 * t] - 127), f1 = NV ? 1.0f : exp2i((int)ref[2 * t + 1] - 127);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);
+                acc[t][n][1] = __fmaf_rn(part[t][n][1], f0, acc[t][n][1]);
+                acc[t][n][2] = __fmaf_rn(part[t][n][2], f1, acc[t][n][2]);
+                acc[t][n][3] = __fmaf_rn(part[t][n][3], f1, acc[t][n][3]);
+            }
+        }
+    }
+}
 
 template <int FMT, int WR, int NT, int BF16OUT>
 __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constant__ Args a)
@@ -110,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
     // ---- the slice's largest |x| per row (after H_k where each thread holds
     // its one unit of x; else before it, |H x| <= sqrt(k) max |x|) ----
     const int units = (s1 - s0) * 4;  // 32-element units per row
-    const bool kept = a.M * units <= kThreads;
+    const bool kept = a.M * units <= kThreads && s1 - s0 <= a.stage;
     auto fetch_x = [&](int m, int64_t k, float *v) {
         uint4 raw[4] = {};
         if (m < a.M && k < a.K) {
@@ -199,73 +288,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
         // steps s0 + wk, s0 + wk + WK, ... (a stage of x is a multiple of WK steps)
         for (int step = st + wk; step < se; step += WK) {
             cp_async_wait<kStages - 2>();
-            const uint32_t at = ring + slot * kStep;
-            load(step + (kStages - 1) * WK, slot == 0 ? kStages - 1 : slot - 1);  // the slot consumed last
+            Piece now;
+            take(ring + slot * kStep, now);
+            load(step + (kStages - 1) * WK, slot == 0 ? kStages - 1 : slot - 1);  // the slot taken last
             slot = slot == kStages - 1 ? 0 : slot + 1;
-            uint32_t w[4][4], sw[4], sc[4][2], ref[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) lds(at + j * 512, w[j], 4);
-            lds(at + 2048, sw, 4);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                if (FMT == FP4_MXFP4) {
-                    ref[j] = max_byte(sw[j]);
-                    sc[j][0] = sc[j][1] = e8m0_rel((sw[j] >> (8 * c)) & 0xFF, ref[j]);
-                } else {
-                    const uint32_t two = (sw[j] >> (16 * (c & 1))) & 0xFFFF;
-                    if (NV) {
-                        const uint32_t f = e4m3x2_to_f16x2(two);
-                        sc[j][0] = __byte_perm(f, 0, 0x1010);
-                        sc[j][1] = __byte_perm(f, 0, 0x3232);
-                    } else {
-                        ref[j] = max_byte(sw[j]);
-                        ref[j] = max(ref[j], __shfl_xor_sync(0xFFFFFFFFu, ref[j], 2));  // the step's other scale word
-                        sc[j][0] = e8m0_rel(two & 0xFF, ref[j]);
-                        sc[j][1] = e8m0_rel(two >> 8, ref[j]);
-                    }
-                }
-            }
-            // the step's own sums: added below with a rounding to nearest, which
-            // the product's accumulation of many steps would not give
-            float part[2][NT][4];
-#pragma unroll
-            for (int t = 0; t < 2; t++)
-#pragma unroll
-                for (int n = 0; n < NT; n++) part[t][n][0] = part[t][n][1] = part[t][n][2] = part[t][n][3] = 0.0f;
-            const uint32_t xb = xs + (step - st) * 256 + c * 16;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint32_t h[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    e2m1x8_to_f16(w[j][i], h[j]);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) h[j][e] = mul_f16x2(h[j][e], sc[j][i >> 1]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    uint32_t bx[4] = {0, 0, 0, 0};
-                    if (8 * n + g < a.cols)
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(bx[0]), "=r"(bx[1]), "=r"(bx[2]), "=r"(bx[3]) : "r"(xb + (8 * n + g) * pitch + i * 64));
-#pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        float *d = part[t][n];
-                        mma_f16(d, h[2 * t][0], h[2 * t + 1][0], h[2 * t][1], h[2 * t + 1][1], bx[0], bx[1]);
-                        mma_f16(d, h[2 * t][2], h[2 * t + 1][2], h[2 * t][3], h[2 * t + 1][3], bx[2], bx[3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < 2; t++) {
-                const float f0 = NV ? 1.0f : exp2i((int)ref[2 * t] - 127), f1 = NV ? 1.0f : exp2i((int)ref[2 * t + 1] - 127);
-#pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);
-                    acc[t][n][1] = __fmaf_rn(part[t][n][1], f0, acc[t][n][1]);
-                    acc[t][n][2] = __fmaf_rn(part[t][n][2], f1, acc[t][n][2]);
-                    acc[t][n][3] = __fmaf_rn(part[t][n][3], f1, acc[t][n][3]);
-                }
-            }
+            multiply_step<FMT, NT, BF16OUT>(now, xs + (step - st) * 256 + c * 16, pitch, a.cols, g, c, acc);
         }
     }
 
@@ -315,35 +342,360 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
     if (cl > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-struct Plan {
-    int wr, cluster, slice, stage;
+// ---- the streamed form -------------------------------------------------------
+// For more columns or larger weights: x is turned to f16 once (prepare_kernel,
+// into the workspace, in the order the lanes read it) instead of by every CTA,
+// and the steps of all tiles form one sequence that is cut evenly over exactly
+// the CTAs that fit on the GPU.  A tile cut between CTAs is summed by the last
+// of them to finish, in CTA order.
+
+struct Stream {
+    uint8_t *xh;         // [cols][pairs * 2 steps][256 bytes]
+    float *x_up;         // [16]
+    unsigned *counters;  // [tiles]
+    float *part;         // [2 * grid][M][128]
+    int pairs;           // pairs of steps per tile
+    int share, more;     // a CTA's pairs of the sequence: share, one more for the first `more` CTAs
+    FastDiv share1_div, share_div, pairs_div;  // by share + 1, share, pairs
 };
 
-// Cuts N into tiles of 32 * wr rows and K into cluster slices.
-static Plan plan(int64_t N, int64_t K, int cols, int sms)
+FP4_DEV uint32_t stream_begin(uint32_t cta, const Stream &s) { return cta * (uint32_t)s.share + min(cta, (uint32_t)s.more); }
+
+// The CTA whose part holds pair q of the sequence.
+FP4_DEV uint32_t stream_owner(uint32_t q, const Stream &s)
 {
+    const uint32_t split = (uint32_t)s.more * ((uint32_t)s.share + 1u);
+    return q < split ? fastdiv(q, s.share1_div) : (uint32_t)s.more + fastdiv(q - split, s.share_div);
+}
+
+// Row blockIdx.x of x: H_k, the power of two, f16 hi (and lo); also zeroes the counters.
+template <int BF16OUT>
+__global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s, int tiles)
+{
+    __shared__ uint32_t top_w[16];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int m = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = m * 512 + threadIdx.x; i < tiles; i += a.M * 512) s.counters[i] = 0;
+    const int units = s.pairs * 8, real = (int)(a.K / 32);
+    float v[32];
+    auto fetch = [&](int u) {
+        uint4 raw[4] = {};
+        if (u < real) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + (int64_t)u * 32);
+#pragma unroll
+            for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
+        }
+        unpack_unit(raw, v);
+        rotate_unit(v, a.hk, a.ck, lane);
+    };
+    uint32_t top = 0;
+    for (int u = threadIdx.x; u < (units + 31) / 32 * 32; u += 512) {
+        fetch(u);
+        top = max(top, __float_as_uint(absmax_tree<32>(v)));
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) top_w[warp] = top;
+    __syncthreads();
+    top = __reduce_max_sync(0xFFFFFFFFu, lane < 16 ? top_w[lane] : 0u);
+    int e = top ? (int)(top >> 23) - 127 - 14 : 0;  // the largest in [2^14, 2^15)
+    e = e < -126 ? -126 : e;
+    const float down = exp2i(-e);
+    if (threadIdx.x == 0) s.x_up[m] = exp2i(e);
+    for (int u = threadIdx.x; u < (units + 31) / 32 * 32; u += 512) {
+        if (units > 512) fetch(u);  // else v still holds the thread's one unit
+        if (u >= units) continue;
+        uint8_t *hi_at = s.xh + ((int64_t)m * s.pairs * 2 + (u >> 2)) * 256 + (u & 3) * 16;
+        uint8_t *lo_at = hi_at + (int64_t)a.M * s.pairs * 512;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float x0 = __fmul_rn(v[8 * q + 2 * j], down), x1 = __fmul_rn(v[8 * q + 2 * j + 1], down);
+                hi[j] = pack_f16(x0, x1);
+                const __half2 hh = *reinterpret_cast<const __half2 *>(&hi[j]);
+                if (!BF16OUT) lo[j] = pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
+            }
+            *reinterpret_cast<uint4 *>(hi_at + q * 64) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (!BF16OUT && a.cols > a.M) *reinterpret_cast<uint4 *>(lo_at + q * 64) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+}
+
+// Shared memory of stream_kernel: every lane's own ring of W, two buffers of XG
+// pairs of x for the CTA (so its warps meet once in XG pairs), the join.
+template <int NT>
+struct StreamShape {
+    static constexpr int ST = NT == 1 ? 4 : 3;
+    static constexpr int XG = 2;
+    static constexpr uint32_t XP = 512 + 64;  // bytes of a column's pair of steps: two columns' pieces fill all banks
+    static constexpr uint32_t XSLOT = 8 * NT * XP;
+    static constexpr uint32_t SMEM = ST * 8 * kStep + 2 * XG * XSLOT + 8 * NT * 512;
+};
+
+template <int FMT, int NT, int BF16OUT>
+__global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s)
+{
+    using S = StreamShape<NT>;
+    constexpr int ST = S::ST, XG = S::XG;
+    constexpr bool NV = FMT == FP4_NVFP4;
+    constexpr uint32_t XP = S::XP, WSLOT = 8 * kStep, XSLOT = S::XSLOT;
+    constexpr int TILES_PER_STEP = FMT == FP4_MXFP4 ? 1 : 2;  // scale tiles along K
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ unsigned arrived;
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int wr = warp & 3, wk = warp >> 2, r0 = wr * 8 + g;
+    const uint32_t ring = smem_u32(smem), mine = ring + warp * kStep + lane * 16, xat = ring + ST * WSLOT;
+    float *red = reinterpret_cast<float *>(smem + ST * WSLOT + 2 * XG * XSLOT);  // [cols][128]
+    const uint32_t begin = stream_begin(blockIdx.x, s), count = stream_begin(blockIdx.x + 1, s) - begin;
+
+    // the stream of loads: this lane's pieces of the next pair's step
+    uint32_t lt = fastdiv(begin, s.pairs_div), ln = 0;
+    int lp = (int)(begin - lt * (uint32_t)s.pairs);
+    const uint8_t *wp[4], *sp;
+    auto aim = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            wp[j] = a.wq + min((int64_t)lt * 128 + r0 + 32 * j, a.N - 1) * (a.K / 2) + (2 * lp + wk) * 64 + c * 16;
+        sp = a.ws + ((int64_t)lt * a.nkb4 + (2 * lp + wk) * TILES_PER_STEP + (FMT == FP4_MXFP4 ? 0 : c >> 1)) * 512 + r0 * 16;
+    };
+    aim();
+    auto load_w = [&](uint32_t slot) {
+        const int step = 2 * lp + wk;
+        // past K: zeros (the second step of a pair, the last step's upper lanes)
+        const bool w_in = step * 128 + c * 32 < (int)a.K, s_in = step * TILES_PER_STEP + (FMT == FP4_MXFP4 ? 0 : c >> 1) < (int)a.nkb4;
+#pragma unroll
+        for (int j = 0; j < 4; j++) cp_async16(mine + slot * WSLOT + j * 512, wp[j], w_in);
+        cp_async16(mine + slot * WSLOT + 2048, sp, s_in);
+    };
+    const uint8_t *xg = s.xh + (int64_t)(threadIdx.x >> 5) * s.pairs * 512 + (threadIdx.x & 31) * 16;
+    const uint32_t xd = xat + (threadIdx.x >> 5) * XP + (threadIdx.x & 31) * 16;
+    uint32_t xn = 0;  // pairs of x asked for
+    int xpair = lp;
+    auto load_x = [&]() {  // the next XG pairs
+#pragma unroll
+        for (int k = 0; k < XG; k++) {
+            if (xn >= count) return;
+            const uint32_t at = xd + (xn % (2 * XG)) * XSLOT;
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+                if (8 * i + (int)(threadIdx.x >> 5) < a.cols) cp_async16(at + i * 8 * XP, xg + ((int64_t)i * 8 * s.pairs + xpair) * 512, true);
+            xn++;
+            xpair = xpair + 1 == s.pairs ? 0 : xpair + 1;
+        }
+    };
+    auto advance = [&]() {
+        ln++;
+        if (++lp == s.pairs) {
+            lp = 0;
+            lt++;
+            if (ln < count) aim();
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; j++) wp[j] += 128;
+            sp += 2 * TILES_PER_STEP * 512;
+        }
+    };
+    // columns that x does not have stay zero
+    for (int i = threadIdx.x; i < 2 * XG * (8 * NT - a.cols) * 32; i += kThreads) {
+        const int slot = i / ((8 * NT - a.cols) * 32), p = i - slot * (8 * NT - a.cols) * 32;
+        *reinterpret_cast<uint4 *>(smem + ST * WSLOT + slot * XSLOT + (a.cols + (p >> 5)) * XP + (p & 31) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    if (!a.w_early) grid_dep_wait();
+#pragma unroll
+    for (int i = 0; i < ST - 1; i++) {
+        if (ln < count) {
+            load_w(i);
+            advance();
+        }
+        if (i == 0) {  // x in the first group
+            if (a.w_early) grid_dep_wait();
+            load_x();
+        }
+        cp_async_commit();
+    }
+
+    float acc[2][NT][4];
+    auto clear = [&]() {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int n = 0; n < NT; n++) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.0f;
+    };
+    clear();
+    uint32_t tile = fastdiv(begin, s.pairs_div);
+    int pair = (int)(begin - tile * (uint32_t)s.pairs), from = pair;
+    uint32_t slot = 0;
+    Piece next;
+    cp_async_wait<ST - 2>();
+    take(mine, next);
+    for (uint32_t n = 0; n < count; n++) {
+        if (n % XG == 0) {
+            __syncthreads();  // these pairs' x has arrived; every warp has left the buffer before
+            load_x();
+            cp_async_commit();
+        }
+        if (ln < count) {  // a lane's ring is its own
+            load_w(slot == 0 ? ST - 1 : slot - 1);
+            advance();
+        }
+        cp_async_commit();
+        slot = slot == ST - 1 ? 0 : slot + 1;
+        cp_async_wait<ST - 2>();  // the next pair's W, and x when that begins a buffer
+        const Piece now = next;
+        take(mine + slot * WSLOT, next);
+        multiply_step<FMT, NT, BF16OUT>(now, xat + (n % (2 * XG)) * XSLOT + wk * 256 + c * 16, XP, 8 * NT, g, c, acc);
+        const bool done = pair == s.pairs - 1;
+        if (done || n == count - 1) {
+            // ---- this CTA's part of the tile ----
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int col = 8 * i + 2 * c + (e & 1);
+                        if (wk && col < a.cols) red[col * 128 + (2 * t + (e >> 1)) * 32 + r0] = acc[t][i][e];
+                    }
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int col = 8 * i + 2 * c + (e & 1);
+                        float *d = red + col * 128 + (2 * t + (e >> 1)) * 32 + r0;
+                        if (!wk && col < a.cols) *d = __fadd_rn(acc[t][i][e], *d);
+                    }
+            __syncthreads();
+            const float gw = NV ? *a.gw : 0.00390625f;  // e8m0_rel's 2^8
+            const bool whole = from == 0 && done;
+            // a CTA has two places for parts: of a tile that its sequence begins in, of a later one
+            float *place = s.part + (int64_t)(2 * blockIdx.x + (begin < tile * (uint32_t)s.pairs)) * a.M * 128;
+            auto store = [&](int i, float v) {
+                const int64_t row = (int64_t)tile * 128 + i % 128;
+                if (row >= a.N) return;
+                if (BF16OUT)
+                    static_cast<__nv_bfloat16 *>(a.out)[(i / 128) * a.ldc + row] = __float2bfloat16_rn(v);
+                else
+                    static_cast<float *>(a.out)[(i / 128) * a.ldc + row] = v;
+            };
+            for (int i = threadIdx.x; i < a.M * 128; i += kThreads) {
+                float t = red[i];
+                if (a.cols > a.M) t = __fadd_rn(t, red[a.M * 128 + i]);
+                t = __fmul_rn(__fmul_rn(t, s.x_up[i / 128]), gw);
+                if (whole)
+                    store(i, t);
+                else
+                    place[i] = t;
+            }
+            if (!whole) {
+                // the last CTA to get here adds all parts, in CTA order
+                const uint32_t q = tile * (uint32_t)s.pairs;
+                const uint32_t first_cta = stream_owner(q, s), last_cta = stream_owner(q + s.pairs - 1, s);
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) arrived = atomicAdd(s.counters + tile, 1u);
+                __syncthreads();
+                if (arrived == last_cta - first_cta) {
+                    __threadfence();
+                    const float *p0 = s.part + (int64_t)(2 * first_cta + (stream_begin(first_cta, s) < q)) * a.M * 128;
+                    const float *p1 = s.part + (int64_t)(2 * first_cta + 2) * a.M * 128;  // the others begin in this tile
+                    for (int i = threadIdx.x; i < a.M * 128; i += kThreads) {
+                        float t = __ldcg(p0 + i);
+#pragma unroll 4
+                        for (uint32_t k = 0; k < last_cta - first_cta; k++) t = __fadd_rn(t, __ldcg(p1 + (int64_t)k * 2 * a.M * 128 + i));
+                        store(i, t);
+                    }
+                }
+            }
+            clear();
+            from = 0;
+        }
+        if (++pair == s.pairs) {
+            pair = 0;
+            tile++;
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// How a call runs: the cheaper of the two forms by a model of the time in
+// microseconds, fitted to sweeps on the B200 (N 447 .. 28672, K 448 .. 14336, M 1
+// .. 16, all formats, every tile width and cluster size: what it picks is within
+// 3 % of the best in most, 1.5 times in the worst, 30 columns of a small weight).
+// Measured, NVFP4: 14336 x 4096, M = 1: tiles of 128 rows in clusters of 2 11.5
+// us, of 64 rows alone 11.6, of 128 rows in clusters of 4 (1.5 rounds of CTAs)
+// 15.6; 28672 x 8192, M = 16: by tiles 69 us, streamed 49; 4096 x 4096, M = 16:
+// 14.4 and 23.
+struct Plan {
+    int wr, cluster, slice, stage;  // by tiles: 32 * wr rows, K cut over a cluster
+    bool streamed;
+    double cost;
+};
+
+// What a step costs with 16 and with 32 columns, against 8.
+static double step_factor(int cols) { return cols <= 8 ? 1.0 : cols <= 16 ? 1.42 : 3.8; }
+
+static Plan plan_tiles(int64_t N, int64_t K, int cols, bool rotated, int sms)
+{
+    // resident CTAs: two per SM, as far as clusters of that size fill a GPC
+    static constexpr double kFill[9] = {0, 1.0, 1.0, 0.95, 0.95, 0.92, 0.89, 0.87, 0.87};
     const int64_t chunks = (K + 127) / 128, atoms = (N + 127) / 128;
     Plan best = {};
-    double least = 0.0;
     for (int wr = 4; wr >= 1; wr /= 2) {
         const int wk = 8 / wr;
         for (int cl = 1; cl <= 8; cl++) {
             const int64_t slice = (chunks + cl - 1) / cl;
             if ((chunks + slice - 1) / slice != cl) continue;  // every CTA has work
-            const int64_t steps = (slice + wk - 1) / wk;
-            const int64_t ctas = atoms * (4 / wr) * cl;
-            const int64_t rounds = (ctas + 2 * sms - 1) / (2 * sms);
-            const double full = (double)std::min<int64_t>(ctas, 2 * (int64_t)sms) / (2.0 * sms);
-            const double cost = rounds * (2.5 + 0.005 * cols * slice + (0.3 + 0.3 * full) * steps);
-            if (best.wr == 0 || cost < least) {
-                least = cost;
-                int64_t stage = (kXBytes / cols - 64) / 256 / wk * wk;
-                stage = std::max<int64_t>(stage, wk);
-                best = {wr, cl, (int)slice, (int)std::min<int64_t>(stage, (slice + wk - 1) / wk * wk)};
-            }
+            const double ctas = (double)(atoms * (4 / wr) * cl), slots = 2.0 * sms * kFill[cl];
+            const double rounds = ctas / slots, whole = floor(rounds), part = rounds - whole;
+            const double turns = rounds <= 1.0 ? 1.0 : whole + (part > 0.0 ? 0.9 + 0.1 * part : 0.0);
+            const double t = (0.45 + 0.66 * std::min(1.0, ctas / (2.0 * sms))) * step_factor(cols);
+            int64_t stage = (kXBytes / cols - 64) / 256 / wk * wk;
+            stage = std::min(std::max<int64_t>(stage, wk), (slice + wk - 1) / wk * wk);
+            // start and end, x to f16, the join of columns and CTAs, the steps, further stages of x
+            const double cost = turns * ((cl == 1 ? 2.4 : 3.5 + 0.02 * cl) + 0.018 * (rotated ? 1.6 : 1.0) * cols * (double)slice + 0.047 * cols +
+                                         0.017 * cols * (cl - 1) + t * (double)((slice + wk - 1) / wk) +
+                                         2.7 * (double)((slice + stage - 1) / stage - 1));
+            if (best.wr == 0 || cost < best.cost) best = {wr, cl, (int)slice, (int)stage, false, cost};
         }
     }
     return best;
+}
+
+static int stream_grid(int64_t total, int cols, int sms) { return (int)std::min<int64_t>(total, (int64_t)sms * (cols > 16 ? 1 : 2)); }
+
+static Plan search(int64_t N, int64_t K, int cols, bool rotated, int sms)
+{
+    Plan p = plan_tiles(N, K, cols, rotated, sms);
+    const int64_t tiles = (N + 127) / 128, pairs = (K + 255) / 256, total = tiles * pairs;
+    if (total >= int64_t(1) << 31) return p;  // the stream's 32-bit sequence; such a weight fits no GPU
+    const double grid = stream_grid(total, cols, sms);
+    // two launches and x, the steps (over 16 columns: one CTA per SM), tiles cut between CTAs
+    const double cost = 10.3 + 0.34 * cols + 0.96 * (cols > 8 && cols <= 16 ? 1.42 : 1.0) * (double)total / grid + 0.17 * cols * grid / (double)tiles;
+    p.streamed = cost < p.cost;
+    /*HOOK*/
+    return p;
+}
+
+// The last search of this thread is kept (a call asks twice, a decode loop again).
+static Plan plan(int64_t N, int64_t K, int cols, bool rotated, int sms)
+{
+    struct Last {
+        int64_t key[5];
+        Plan p;
+    };
+    static thread_local Last last = {{-1, -1, -1, -1, -1}, {}};
+    const int64_t key[5] = {N, K, cols, rotated, sms};
+    if (!std::equal(key, key + 5, last.key)) {
+        last.p = search(N, K, cols, rotated, sms);
+        std::copy(key, key + 5, last.key);
+    }
+    return last.p;
 }
 
 template <int FMT, int WR, int NT, int BF16OUT>
@@ -391,11 +743,64 @@ static cudaError_t launch_f(const Args &a, const Plan &p, cudaStream_t st)
     return cudaErrorInvalidValue;
 }
 
+// Workspace of the streamed form, and its sizes.
+struct Layout {
+    size_t x_up, counters, part, total;
+    int64_t tiles;
+    int pairs, grid;
+};
+
+static Layout layout(int64_t M, int64_t N, int64_t K, int cols, int sms)
+{
+    Layout l;
+    l.tiles = (N + 127) / 128;
+    l.pairs = (int)((K + 255) / 256);
+    l.grid = stream_grid(l.tiles * l.pairs, cols, sms);
+    auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+    l.x_up = up((size_t)cols * l.pairs * 512);
+    l.counters = l.x_up + 256;
+    l.part = l.counters + up((size_t)l.tiles * 4);
+    l.total = l.part + (size_t)2 * l.grid * M * 128 * 4;
+    return l;
+}
+
+template <int FMT, int NT, int BF16OUT>
+static cudaError_t stream_t(const Args &a, const Stream &s, int64_t tiles, int grid, cudaStream_t st)
+{
+    auto kern = stream_kernel<FMT, NT, BF16OUT>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kMaxSmem, done);
+    if (e != cudaSuccess) return e;
+    e = launch_k(prepare_kernel<BF16OUT>, dim3((unsigned)a.M), dim3(512), 0, st, true, a, s, (int)tiles);
+    if (e != cudaSuccess) return e;
+    constexpr size_t smem = StreamShape<NT>::SMEM;
+    return launch_k(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, true, a, s);
+}
+
+template <int FMT, int BF16OUT>
+static cudaError_t stream_f(const Args &a, void *ws, int sms, cudaStream_t st)
+{
+    const Layout l = layout(a.M, a.N, a.K, a.cols, sms);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    const int share = (int)(l.tiles * l.pairs / l.grid), more = (int)(l.tiles * l.pairs % l.grid);
+    const Stream s = {base, reinterpret_cast<float *>(base + l.x_up), reinterpret_cast<unsigned *>(base + l.counters),
+                      reinterpret_cast<float *>(base + l.part), l.pairs, share, more, make_fastdiv((uint32_t)share + 1),
+                      make_fastdiv((uint32_t)share), make_fastdiv((uint32_t)l.pairs)};
+    if (a.cols <= 8) return stream_t<FMT, 1, BF16OUT>(a, s, l.tiles, l.grid, st);
+    if (a.cols <= 16) return stream_t<FMT, 2, BF16OUT>(a, s, l.tiles, l.grid, st);
+    return stream_t<FMT, BF16OUT ? 2 : 4, BF16OUT>(a, s, l.tiles, l.grid, st);
+}
+
 }  // namespace w4
+
+size_t linear_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K, int cols, bool rotated, int sms)
+{
+    return M > 0 && N > 0 && K > 0 && w4::plan(N, K, cols, rotated, sms).streamed ? w4::layout(M, N, K, cols, sms).total : 0;
+}
 
 cudaError_t launch_linear_w4a16(const uint16_t *x, int64_t ldx, int64_t M, int64_t K, int fmt, int hk, float ck,
                                 const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N, int bf16out, void *C,
-                                int64_t ldc, int w_early, int sms, cudaStream_t st)
+                                int64_t ldc, int w_early, void *ws, int sms, cudaStream_t st)
 {
     w4::Args a = {};
     a.x = x;
@@ -414,7 +819,12 @@ cudaError_t launch_linear_w4a16(const uint16_t *x, int64_t ldx, int64_t M, int64
     a.ldc = ldc;
     a.chunks = (int)((K + 127) / 128);
     a.w_early = w_early;
-    const w4::Plan p = w4::plan(N, K, a.cols, sms);
+    const w4::Plan p = w4::plan(N, K, a.cols, hk != 0, sms);
+    if (p.streamed) {
+        if (fmt == FP4_MXFP4) return bf16out ? w4::stream_f<FP4_MXFP4, 1>(a, ws, sms, st) : w4::stream_f<FP4_MXFP4, 0>(a, ws, sms, st);
+        if (fmt == FP4_NVFP4) return bf16out ? w4::stream_f<FP4_NVFP4, 1>(a, ws, sms, st) : w4::stream_f<FP4_NVFP4, 0>(a, ws, sms, st);
+        return bf16out ? w4::stream_f<FP4_MXFP4_16, 1>(a, ws, sms, st) : w4::stream_f<FP4_MXFP4_16, 0>(a, ws, sms, st);
+    }
     a.cluster = p.cluster;
     a.slice = p.slice;
     a.stage = p.stage;

@@ -480,6 +480,10 @@ fp4_status fp4_paged_attention(const fp4_kv_cache *cache, const void *q, int64_t
                                float scale, int64_t window, int out_dtype, void *out, float *lse, void *workspace,
                                size_t ws_bytes, void *stream);
 
+/* Bytes of device scratch fp4_linear_w4a16 needs for these sizes, whatever its
+ * other arguments (0 when none).  Host-only. */
+fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int fmt, size_t *bytes);
+
 /*
  * fp4_linear_w4a16 — the weight-only linear layer of a decode step (M <= 16):
  * C = H_k(x) W^T with FP4 weights and activations that stay in 16 bits, for
@@ -490,11 +494,14 @@ fp4_status fp4_paged_attention(const fp4_kv_cache *cache, const void *q, int64_t
  * row's largest lose bits); rotated ones are rounded to 11 bits for bf16
  * output and to 22 for fp32.  E8M0 scales more than 2^22 below the largest of
  * their row's 128 elements count as zero.  fp32 sums in a fixed order.
- * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch, no workspace.
+ *   workspace  at least fp4_linear_w4a16_workspace_size() bytes, 256-byte
+ *           aligned (NULL when that is 0); its contents on entry do not matter.
+ * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch for few rows, two
+ * otherwise; results repeat bit for bit.
  */
 fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
                             const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,
-                            int out_dtype, void *C, int64_t ldc, void *stream);
+                            int out_dtype, void *C, int64_t ldc, void *workspace, size_t ws_bytes, void *stream);
 
 /* Number of kernels this library has launched in this process so far
  * (host-side counter; diagnostics and launch accounting). */

@@ -133,10 +133,10 @@ def test_attention_workspace(L):
 
 
 def linear(L, **kw):
-    a = dict(x=F, M=4, K=256, ldx=256, fmt=1, hk=0, opts=None, wq=F, ws=F, gw=F, N=64, out=1, c=F, ldc=64)
+    a = dict(x=F, M=4, K=256, ldx=256, fmt=1, hk=0, opts=None, wq=F, ws=F, gw=F, N=64, out=1, c=F, ldc=64, wsp=None, wsb=0)
     a.update(kw)
     return L.fp4_linear_w4a16(a["x"], a["M"], a["K"], a["ldx"], a["fmt"], a["hk"], a["opts"], a["wq"], a["ws"], a["gw"],
-                              a["N"], a["out"], a["c"], a["ldc"], None)
+                              a["N"], a["out"], a["c"], a["ldc"], a["wsp"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -144,10 +144,25 @@ def linear(L, **kw):
     (dict(fmt=4), 2), (dict(hk=48), 2), (dict(hk=128, K=320, ldx=320), 2), (dict(out=3), 1), (dict(x=None), 1),
     (dict(wq=None), 1), (dict(ws=None), 1), (dict(c=None), 1), (dict(gw=None), 1), (dict(x=F + 8), 3), (dict(ldx=260), 3),
     (dict(wq=F + 8), 3), (dict(ws=F + 4), 3), (dict(c=F + 4), 3), (dict(gw=F + 2), 3),
+    (dict(M=16, N=28672, K=8192, ldx=8192, ldc=28672), 1),
+    (dict(M=16, N=28672, K=8192, ldx=8192, ldc=28672, wsp=F, wsb=64), 1),
+    (dict(M=16, N=28672, K=8192, ldx=8192, ldc=28672, wsp=F + 16, wsb=1 << 40), 3),
     (dict(N=(1 << 30) + 1, ldc=1 << 31), 2), (dict(K=1 << 31, ldx=1 << 31), 2), (dict(M=0), 0), (dict(N=0, ldc=0), 0),
 ])
 def test_linear_refuses(L, kw, code):
     assert linear(L, **kw) == code
+
+
+def test_linear_workspace(L):
+    b = ctypes.c_size_t()
+    size = L.fp4_linear_w4a16_workspace_size
+    assert size(16, 28672, 8192, 1, ctypes.byref(b)) == 0 and b.value >= 16 * 8192 * 2
+    assert size(1, 1024, 4096, 1, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(0, 4096, 4096, 1, ctypes.byref(b)) == 0 and b.value == 0
+    assert size(17, 4096, 4096, 1, ctypes.byref(b)) == 2
+    assert size(1, 4096, 4096, 3, ctypes.byref(b)) == 2
+    assert size(-1, 4096, 4096, 1, ctypes.byref(b)) == 1
+    assert size(1, 4096, 4096, 1, None) == 1
 
 
 def test_linear_options(L):
