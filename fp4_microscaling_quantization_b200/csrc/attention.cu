@@ -10,30 +10,39 @@
 // unnormalised o are rescaled when m grows.
 //
 // What bounds it: the cache is read once, 2 * dim * (1/2 + 1/block) bytes per
-// token and head, and every element has to become a 16-bit operand first:
-// the issue slots of that conversion come next after HBM.  So:
+// token and head, and every element has to become a 16-bit operand first: the
+// issue slots of that conversion come next after HBM.  Per 32 tokens of a head
+// of 128 (4608 bytes, 198 clocks of an SM's share of HBM) a warp issues about
+// 560 instructions, 128 of them conversions (64 a clock and SM) and 128 scale
+// multiplies, and at 16 warps per SM about 0.6 slots of a clock are used: 65 %
+// of the measured copy rate for one sequence of 262143 tokens (MXFP4, 67 us),
+// 59 % for 64 of 1 to 8192 (NVFP4, 80 us).  So:
 //   * The products run on mma.sync m16n8k16 (f16 in, fp32 sums) from registers.
 //     tcgen05 would need the dequantized tile written to shared or tensor
 //     memory first, at four times the packed bytes; its rate is not what
 //     is short here (up to 8 query rows per key head).
 //   * The order of a product's inner index is free, so each lane's operand
-//     elements are whole consecutive bytes of a token's row: K is the B operand
-//     (8 tokens a tile, a lane holds dim/4 consecutive elements of one token),
-//     V the A operand (a lane holds dim/8 consecutive elements of 4 tokens).
-//     A byte of K is a register pair after one conversion; two tokens' V
-//     bytes are merged nibble by nibble first.  The scores' result registers
-//     are then the next product's B operand as they are: nothing is exchanged.
+//     elements are whole consecutive bytes of a token's row.  K is the row
+//     operand of the scores (a lane holds dim/4 consecutive elements of two
+//     tokens), q the 8 columns; V transposed is the row operand of the output
+//     (a lane holds dim/8 consecutive elements of 4 tokens), the weights the
+//     columns.  A byte of K is a register pair after one conversion; two
+//     tokens' V bytes are merged nibble by nibble first.  The scores' result
+//     becomes the next product's operand by one 8 x 8 transpose of registers.
+//     (K as the column operand needs no transpose, but half of its rows are
+//     padding: 98.7 us instead of 87.4 for the batch above, at that stage.)
 //   * E2M1 times its block scale is exact in f16: for NVFP4 the E4M3 scale
 //     itself (6 significant bits, 2^-10 .. 2688), for E8M0 a power of two
 //     relative to the largest scale that the warp has met so far.
-//   * q in f16 as a power of two times hi + lo: query rows 0-7 of the product
-//     hold hi and rows 8-15 lo, so 22 bits cost nothing for groups of up to 8.
-//     Weights w_t are rounded to f16 (11 bits, scaled by 2^15 so that they
-//     stay normal down to 2^-29 of the largest; below, to steps of 2^-39), and
-//     for fp32 output are split into hi + lo as well, a second product.
-//   * Every warp streams its own steps of 16, 32 or 64 tokens through its own ring
-//     of cp.async stages: no barrier among warps until their results are
-//     joined.  Rows lie swizzled, so all operand loads are free of bank conflicts.
+//   * q in f16 as a power of two times hi: exact for a bf16 q, and hi + lo (a
+//     second product) after a rotation.  Weights w_t are rounded to f16 (11
+//     bits, scaled by 2^15 so that they stay normal down to 2^-29 of the
+//     largest; below, to steps of 2^-39), and for fp32 output are split into
+//     hi + lo as well.
+//   * Every warp streams its own steps of 16, 32 or 64 tokens through its own
+//     two stages of asynchronous copies: no barrier among warps until their
+//     results are joined.  (Three or four stages, and scores computed beside
+//     the values of the step before, were no faster: 84.3 against 86.0 and 86.3.)
 // Long sequences are cut into chunks of tokens over CTAs; a second kernel
 // joins the chunks.  The cut depends on the call's sizes only, and every sum
 // has a fixed order, so results repeat bit for bit.
@@ -83,12 +92,12 @@ struct Shape {
     static constexpr int QB = D / 2;                             // element bytes per row
     static constexpr int TS = D == 64 ? 64 : D == 128 ? 32 : 16; // tokens per step
     static constexpr int STAGE = 2 * TS * (QB + SB);             // bytes: K, V elements, K, V scales
-    static constexpr int ST = 3;                                 // stages per warp
+    static constexpr int ST = 2;                                 // stages per warp
     static constexpr int RING = NW * ST * STAGE;
     static constexpr int JOIN = NW * HT * D * 4;                 // the warps' results, over the ring
     static constexpr int QF = 2 * HT * D * 2;                    // hi and lo of q
     // q lies in warp 0's last stage, which its first loop trip fills, where it
-    // fits (dim 64, 128: a fourth CTA per SM), else behind the ring
+    // fits (dims 64, 128), else behind the ring
     static constexpr int BODY = RING > JOIN ? RING : JOIN;
     static constexpr int QAT = QF <= STAGE ? (ST - 1) * STAGE : BODY;
     static constexpr int SMEM = QF <= STAGE ? BODY : BODY + QF;
@@ -107,6 +116,15 @@ FP4_DEV uint32_t transpose_8x8(uint32_t v)
 {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// The bits of a where m is set, of b elsewhere: one instruction (written out,
+// the compiler moves the masks before the shifts and needs two).
+FP4_DEV uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
     return r;
 }
 
@@ -185,7 +203,7 @@ FP4_DEV void write_rows(const float *o, int rows, int64_t out_row, const Args &a
 // ROT: the cache is rotated, so q has more than f16's 11 bits and its lo rows
 // are not zero (a bf16 q is exact in the hi rows alone).
 template <int FMT, int D, int BF16OUT, bool ROT>
-__global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_kernel(const __grid_constant__ Args a)
 {
     using S = Shape<FMT, D>;
     constexpr int WPT = D / 32;       // words of a lane's K row part
@@ -213,24 +231,28 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
 
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * S::ST * S::STAGE);
     const int32_t *table = a.table + b * a.table_b;
-    const uint32_t pm = (1u << a.c.page_shift) - 1u;
+    const uint32_t pm = (1u << a.c.page_shift) - 1u;  // tokens of a page, less one
 
     // ---- the stream of this warp's steps ----
-    // Page numbers of 32 half steps at a time, one per lane, loaded 32 ahead.
+    // The cache rows (page, head, position) of 32 half steps at a time, one per
+    // lane, whose pages are loaded 32 ahead.  Rows are 32-bit: 2^32 of them are
+    // more than device memory holds.
     const int first = cs + warp * S::TS;
     constexpr int PAGED = 32 / HALVES;  // steps per batch
-    auto pages_at = [&](int step) -> int {
-        const int t = first + (step + lane / HALVES) * (NW * S::TS) + 16 * (lane % HALVES);
-        return t < ce ? __ldg(table + (t >> a.c.page_shift)) : -1;
+    auto token_at = [&](int step) { return first + (step + lane / HALVES) * (NW * S::TS) + 16 * (lane % HALVES); };
+    auto page_at = [&](int t) -> int { return t < ce ? __ldg(table + (t >> a.c.page_shift)) : -1; };
+    uint32_t row_now, bad_now;
+    auto rows_of = [&](int page, int t) {
+        const bool live = (uint32_t)page < (uint32_t)a.c.num_pages;  // num_pages < 2^31
+        bad_now = __ballot_sync(0xFFFFFFFFu, !live);
+        row_now = live ? (((uint32_t)page * (uint32_t)a.c.heads + kvh) << a.c.page_shift) + ((uint32_t)t & pm) : 0u;
     };
-    int page_now = pages_at(0), page_next = pages_at(PAGED);
-    uint32_t bad_now = __ballot_sync(0xFFFFFFFFu, (uint32_t)page_now >= (uint32_t)a.c.num_pages);  // num_pages < 2^31
-    if ((bad_now >> lane) & 1u) page_now = 0;
-    // this lane's pieces of a page: one 64-bit multiply-add per array and page
-    const uint32_t page_q = (uint32_t)(a.c.heads << a.c.page_shift) * S::QB, page_s = (uint32_t)(a.c.heads << a.c.page_shift) * S::SB;
-    const uint8_t *kq_lane = a.c.kq + (uint32_t)(kvh << a.c.page_shift) * S::QB + lane * 16;
-    const uint8_t *vq_lane = a.c.vq + (uint32_t)(kvh << a.c.page_shift) * S::QB + lane * 16;
-    const uint8_t *s_lane = (lane < 16 ? a.c.ks : a.c.vs) + (uint32_t)(kvh << a.c.page_shift) * S::SB + (lane & 15) * 16;
+    int page_next = page_at(token_at(0));
+    rows_of(page_next, token_at(0));
+    page_next = page_at(token_at(PAGED));
+    // this lane's pieces of a row's 16 tokens
+    const uint8_t *kq_lane = a.c.kq + lane * 16, *vq_lane = a.c.vq + lane * 16;
+    const uint8_t *s_lane = (lane < 16 ? a.c.ks : a.c.vs) + (lane & 15) * 16;
     uint32_t k_dst[D == 256 ? PIECES / 2 : 1], v_dst[D == 256 ? PIECES / 2 : 1];  // dim 256: swizzled
 #pragma unroll
     for (int i = 0; i < (D == 256 ? PIECES / 2 : 1); i++) {
@@ -239,38 +261,20 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
         v_dst[i] = ring + S::TS * S::QB + v_piece<D>(t, j);
     }
     const uint32_t s_dst = ring + 2 * S::TS * S::QB + (lane < 16 ? 0 : S::TS * S::SB) + (lane & 15) * 16;
-    const bool small_pages = (1 << a.c.page_shift) < S::TS;
     uint32_t holes = 0;  // bit 4 * stage + half: no page
     auto fetch = [&](int step, int stage) {
         const int i0 = step % PAGED;
         if (i0 == 0 && step) {
-            page_now = page_next;
-            page_next = pages_at(step + PAGED);
-            bad_now = __ballot_sync(0xFFFFFFFFu, (uint32_t)page_now >= (uint32_t)a.c.num_pages);
-            if ((bad_now >> lane) & 1u) page_now = 0;
+            rows_of(page_next, token_at(step));
+            page_next = page_at(token_at(step + PAGED));
         }
         const uint32_t bad = (bad_now >> (i0 * HALVES)) & ((1u << HALVES) - 1u);
         holes = (holes & ~(15u << (4 * stage))) | (bad << (4 * stage));
         const uint32_t so = (uint32_t)(stage * S::STAGE);
-        const uint32_t pos = (uint32_t)(first + step * (NW * S::TS)) & pm;
-        uint32_t page = __shfl_sync(0xFFFFFFFFu, page_now, i0 * HALVES);
-        const uint8_t *kq = kq_lane + (uint64_t)page * page_q + pos * S::QB, *vq = vq_lane + (uint64_t)page * page_q + pos * S::QB;
-        const uint8_t *sc = s_lane + (uint64_t)page * page_s + pos * S::SB;
 #pragma unroll
         for (int h = 0; h < HALVES; h++) {
-            if (h > 0) {
-                if (small_pages) {  // a step of several pages
-                    page = __shfl_sync(0xFFFFFFFFu, page_now, i0 * HALVES + h);
-                    const uint32_t p = (pos + 16 * h) & pm;
-                    kq = kq_lane + (uint64_t)page * page_q + p * S::QB;
-                    vq = vq_lane + (uint64_t)page * page_q + p * S::QB;
-                    sc = s_lane + (uint64_t)page * page_s + p * S::SB;
-                } else {
-                    kq += 16 * S::QB;
-                    vq += 16 * S::QB;
-                    sc += 16 * S::SB;
-                }
-            }
+            const uint32_t row = __shfl_sync(0xFFFFFFFFu, row_now, i0 * HALVES + h);
+            const uint8_t *kq = kq_lane + (uint64_t)row * S::QB, *vq = vq_lane + (uint64_t)row * S::QB;
             const bool live = !((bad >> h) & 1u);
 #pragma unroll
             for (int i = 0; i < PIECES / 2; i++) {
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
                 cp_async16((D == 256 ? v_dst[i] : k_dst[0] + S::TS * S::QB + i * 512) + so + h * 16 * S::QB, vq + i * 512, live);
             }
             if ((lane & 15) < S::SB)  // 16 rows' scales: SB pieces of K by the lower lanes, of V by the upper
-                cp_async16(s_dst + so + h * 16 * S::SB, sc, live);
+                cp_async16(s_dst + so + h * 16 * S::SB, s_lane + (uint64_t)row * S::SB, live);
         }
     };
 #pragma unroll
@@ -357,7 +361,8 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
         vs_at[i] = 2 * S::TS * S::QB + S::TS * S::SB + tau(2 * c + i) * S::SB + vsj;
     }
 
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+    // no score yet: the least finite number, so that differences stay numbers
+    float m_run[2] = {-kFltMax, -kFltMax}, l_run[2] = {0.0f, 0.0f};
     uint32_t k_ref = 0, v_ref = 0;  // E8M0: the largest scale bytes so far
     float acc[MT][4];
 #pragma unroll
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
             float alpha[2];
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                alpha[i] = m_new[i] > m_run[i] ? ex2(__fsub_rn(m_run[i], m_new[i])) : 1.0f;  // 0 from -inf
+                alpha[i] = m_new[i] > m_run[i] ? ex2(__fsub_rn(m_run[i], m_new[i])) : 1.0f;  // 0 at first
                 l_run[i] = __fmul_rn(l_run[i], alpha[i]);
                 alpha[i] = __fmul_rn(alpha[i], f);
                 m_run[i] = m_new[i];
@@ -523,8 +528,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
             }
             v_ref = ref_new;
         }
-        const float off0 = __fsub_rn(kPShift, m_run[0] == -INFINITY ? 0.0f : m_run[0]);
-        const float off1 = __fsub_rn(kPShift, m_run[1] == -INFINITY ? 0.0f : m_run[1]);
+        const float off0 = __fsub_rn(kPShift, m_run[0]), off1 = __fsub_rn(kPShift, m_run[1]);
 #pragma unroll
         for (int j = 0; j < NT / 2; j++) {
 #pragma unroll
@@ -571,10 +575,10 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
             for (int i = 0; i < VW; i++) {
                 const uint32_t M = 0x0F0F0F0Fu;
                 uint32_t a0[4], a1[4], a2[4], a3[4];
-                e2m1x8_to_f16((w[0][i] & M) | ((w[1][i] << 4) & ~M), a0);
-                e2m1x8_to_f16(((w[0][i] >> 4) & M) | (w[1][i] & ~M), a1);
-                e2m1x8_to_f16((w[2][i] & M) | ((w[3][i] << 4) & ~M), a2);
-                e2m1x8_to_f16(((w[2][i] >> 4) & M) | (w[3][i] & ~M), a3);
+                e2m1x8_to_f16(select_bits(w[0][i], w[1][i] << 4, M), a0);
+                e2m1x8_to_f16(select_bits(w[0][i] >> 4, w[1][i], M), a1);
+                e2m1x8_to_f16(select_bits(w[2][i], w[3][i] << 4, M), a2);
+                e2m1x8_to_f16(select_bits(w[2][i] >> 4, w[3][i], M), a3);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     a0[k] = mul_f16x2(a0[k], s01[i >> 1]);
@@ -588,29 +592,22 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
         }
     };
 
-    // A step's scores are computed beside the values of the step before it: two
-    // independent chains for the scheduler.
-    if (first < ce) {
-        cp_async_wait<S::ST - 2>();
+    // two steps to a trip: stages are then constants in all addresses
+    static_assert(S::ST == 2, "one stage is read while the other is filled");
+    auto advance = [&](int t0, int step, int stage) {
+        cp_async_wait<0>();
         __syncwarp();
-        look(first, 0);
-        scores(0);
-        int stage = 0, step = 0;
-        for (int t0 = first + NW * S::TS; t0 < ce; t0 += NW * S::TS, step++) {
-            const int next = stage == S::ST - 1 ? 0 : stage + 1;
-            weights();
-            // into the stage of the step before this one, which all lanes have left
-            if (t0 + (S::ST - 2) * NW * S::TS < ce) fetch(step + S::ST - 1, stage == 0 ? S::ST - 1 : stage - 1);
-            cp_async_commit();
-            cp_async_wait<S::ST - 2>();  // the next step's copies
-            __syncwarp();
-            look(t0, next);
-            scores(next);
-            values(stage);
-            stage = next;
-        }
+        // into the stage of the step before this one, which all lanes have left
+        if (t0 + NW * S::TS < ce) fetch(step + 1, stage ^ 1);
+        cp_async_commit();
+        look(t0, stage);
+        scores(stage);
         weights();
         values(stage);
+    };
+    for (int t0 = first, step = 0; t0 < ce; t0 += 2 * NW * S::TS, step += 2) {
+        advance(t0, step, 0);
+        if (t0 + NW * S::TS < ce) advance(t0 + NW * S::TS, step + 1, 1);
     }
 
     // ---- join the warps ----
@@ -643,7 +640,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? 2 : 4) paged_kernel(const 
         for (int w = 1; w < NW; w++) m = fmaxf(m, sm_m[w][h]);
 #pragma unroll
         for (int w = 0; w < NW; w++) {
-            f[w] = sm_m[w][h] == -INFINITY ? 0.0f : ex2(__fsub_rn(sm_m[w][h], m));
+            f[w] = ex2(__fsub_rn(sm_m[w][h], m));  // without a score l is 0
             l = __fmaf_rn(f[w], sm_l[w][h], l);
         }
         const int64_t row = (int64_t)b * a.q_heads + h0 + h;
@@ -696,7 +693,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     const Range r = live_range(a, b);
     const int n = r.end > r.base ? (int)((r.end - r.base + a.chunk - 1) / a.chunk) : 0;
     const float2 *ml = a.part_ml + row * a.chunks;
-    float m = -INFINITY;
+    float m = -kFltMax;
     for (int i = threadIdx.x; i < n; i += 128) {
         f[i] = ml[i].x;
         m = fmaxf(m, f[i]);
@@ -708,7 +705,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     float l = 0.0f;
     for (int i = threadIdx.x; i < n; i += 128) {
-        f[i] = f[i] == -INFINITY ? 0.0f : ex2(__fsub_rn(f[i], m));
+        f[i] = ex2(__fsub_rn(f[i], m));
         l = __fmaf_rn(f[i], ml[i].y, l);
     }
 #pragma unroll

@@ -104,6 +104,8 @@ fp4_status kv_geometry(int64_t num_pages, int page_size, int kv_heads, int head_
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FP4_ERR_UNSUPPORTED;
     if (hadamard_k && head_dim % hadamard_k) return FP4_ERR_UNSUPPORTED;
     if (kv_heads > 65535 || num_pages > (int64_t(1) << 31) - 1) return FP4_ERR_UNSUPPORTED;
+    // head rows have 32-bit numbers: 2^32 of the smallest are more than device memory holds
+    if (num_pages * kv_heads > ((int64_t(1) << 32) - 1) / page_size) return FP4_ERR_UNSUPPORTED;
     return FP4_OK;
 }
 

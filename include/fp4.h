@@ -393,6 +393,7 @@ fp4_status fp4_gemm_decode_noalloc(const uint8_t *Aq, const uint8_t *As, const f
  *               held rotated by H_k along head_dim ("FP4 quantization analysis:
  *               MXFP4 vs NVFP4" §3.2.3); every call below takes and returns
  *               unrotated values.
+ *   num_pages * kv_heads * page_size below 2^32 (more than memory holds).
  *   kq, ks, vq, vs 16-byte aligned.  Errors: FP4_ERR_INVALID_ARG (null
  *   pointers, negative sizes), FP4_ERR_UNSUPPORTED (fmt, page_size, head_dim,
  *   hadamard_k outside these), FP4_ERR_ALIGNMENT.

@@ -76,7 +76,8 @@ def test_cache_sizes(L):
     assert q.value == 10 * 16 * 8 * 64 and s.value == 10 * 16 * 8 * 8
     assert L.fp4_kv_cache_sizes(10, 64, 3, 64, 0, *p) == 0 and s.value == 10 * 64 * 3 * 2
     assert L.fp4_kv_cache_sizes(0, 64, 3, 64, 2, *p) == 0 and q.value == 0
-    assert L.fp4_kv_cache_sizes(1 << 30, 256, 8, 256, 2, *p) == 0 and q.value == (1 << 30) * 256 * 8 * 128
+    assert L.fp4_kv_cache_sizes(1 << 20, 256, 8, 256, 2, *p) == 0 and q.value == (1 << 20) * 256 * 8 * 128
+    assert L.fp4_kv_cache_sizes(1 << 21, 256, 8, 256, 2, *p) == 2  # 2^32 rows
     assert L.fp4_kv_cache_sizes(10, 24, 8, 128, 1, *p) == 2
     assert L.fp4_kv_cache_sizes(10, 16, 8, 100, 1, *p) == 2
     assert L.fp4_kv_cache_sizes(10, 16, 8, 128, 1, None, ctypes.byref(s)) == 1
