@@ -37,7 +37,8 @@ def _fmt(fmt) -> int:
 
 
 def _stream_handle(torch, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The current stream of a device (a tensor's, or an ordinal)."""
+    return torch._C._cuda_getCurrentRawStream(device if isinstance(device, int) else device.index)
 
 
 def _run(name: str, device, *args) -> None:

@@ -98,6 +98,34 @@ def test_strided_inputs(fp4, orc, fmt, dim):
         assert np.array_equal(got.cpu().numpy(), oracle_rows(orc, x.cpu().contiguous(), fmt, 0, 0, 0, g)[2])
 
 
+@pytest.mark.parametrize("offset,pad", [(8, 0), (0, 8), (16, 16)])
+def test_alignment_of_rows(fp4, orc, offset, pad):
+    """Rows at 16 and at 32 bytes: both widths of load."""
+    import torch
+    T, H, D = 11, 3, 64
+    buf = draw((T * (H * D + pad) + offset,), 6).cuda()
+    k = buf[offset:].as_strided((T, H, D), (H * D + pad, D, 1))
+    assert k.data_ptr() % 32 == (16 if offset == 8 else 0)
+    cache = fp4.KVCache.empty(1, H, 16, D, MX)
+    slots = torch.arange(T, device="cuda")
+    fp4.kv_append(cache, k, k, slots)
+    got = fp4.kv_gather(cache, slots, out_dtype=fp4.FP4_OUT_F32)
+    want = oracle_rows(orc, k.cpu().contiguous(), MX, 0, 0, 0, 1.0)[2]
+    assert np.array_equal(got[0].cpu().numpy(), want) and np.array_equal(got[1].cpu().numpy(), want)
+
+
+def test_many_tokens(fp4, orc):
+    """Enough for K and V to share their threads (one grid row)."""
+    import torch
+    T, H, D = 5003, 4, 128
+    k, v = draw((T, H, D), 14), draw((T, H, D), 15)
+    cache = fp4.KVCache.empty(-(-T // 64), H, 64, D, NV, GK, GV, 64)
+    slots = torch.randperm(cache.num_pages * 64, generator=torch.Generator().manual_seed(16))[:T].cuda()
+    fp4.kv_append(cache, k.cuda(), v.cuda(), slots)
+    for got, x, g in zip(fp4.kv_gather(cache, slots, out_dtype=fp4.FP4_OUT_F32), (k, v), (GK, GV)):
+        assert np.array_equal(got.cpu().numpy(), oracle_rows(orc, x, NV, 64, 0, 0, g)[2])
+
+
 def test_slots_outside_are_dropped_and_read_as_zeros(fp4):
     import torch
     cache = new_cache(fp4, 2, 2, 16, 64, NV, 16)

@@ -177,6 +177,65 @@ def test_weights_static_and_graph(fp4):
     assert torch.equal(out, want) and torch.equal(again, want)
 
 
+# sizes that run as one stream over all CTAs (a workspace is asked for): odd
+# numbers of steps, a ragged last tile, tiles cut between two and many CTAs,
+# 8, 16 and 32 columns
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("M,N,K,hk", [(6, 28672, 4128, 32), (16, 20011, 4128, 0), (9, 8192, 14336, 128), (12, 23353, 1536, 128)])
+def test_streamed(fp4, fmt, M, N, K, hk):
+    import torch
+    assert fp4.linear_w4a16_workspace_size(M, N, K, fmt) > 0
+    x, w = inputs(M, N, K, M + hk)
+    W = fp4.quantize(w, fmt, hadamard_k=hk)
+    want = check(fp4, x, W, fmt, hk, N)
+    # a workspace full of anything, used again, and early weight loads
+    ws = torch.full((fp4.linear_w4a16_workspace_size(M, N, K, fmt),), 0xFF, dtype=torch.uint8, device="cuda")
+    for static in (False, True, True):
+        got = fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, out_dtype=fp4.FP4_OUT_F32, workspace=ws, weights_static=static)
+        assert torch.equal(got, want)
+
+
+def test_streamed_graphs_share_a_workspace(fp4):
+    """Two graphs of one stream with one workspace, replayed in turn; two
+    streams at once with a workspace each."""
+    import torch
+    M, N, K = 16, 20011, 4128
+    ws = torch.empty(fp4.linear_w4a16_workspace_size(M, N, K, NV), dtype=torch.uint8, device="cuda")
+    sides = []
+    for seed in (1, 2):
+        x, w = inputs(M, N, K, seed)
+        W = fp4.quantize(w, NV)
+        want = fp4.linear_w4a16(x, W, NV)
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fp4.linear_w4a16(x, W, NV, out=out, workspace=ws)
+        sides.append((g, x, W, out, want))
+    for _ in range(3):
+        for g, _, _, out, _ in sides:
+            out.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for _, _, _, out, want in sides)
+    streams, outs = [torch.cuda.Stream() for _ in sides], []
+    for _ in range(4):
+        for st, (_, x, W, _, want) in zip(streams, sides):
+            with torch.cuda.stream(st):
+                outs.append((fp4.linear_w4a16(x, W, NV), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 256, 32768), (1, 128, 65536), (4, 130, 16384), (8, 64, 32768), (16, 40, 32768), (16, 200, 4096)])
+def test_long_slices(fp4, M, N, K):
+    """Slices of x longer than the part of it that is held at a time, hi and lo
+    columns among them."""
+    x, w = inputs(M, N, K, 11)
+    check(fp4, x, fp4.quantize(w, NV, hadamard_k=64), NV, 64, N)
+    check(fp4, x, fp4.quantize(w, MX), MX, 0, N)
+
+
 def test_empty(fp4):
     import torch
     x, w = inputs(1, 128, 64, 10)

@@ -224,6 +224,95 @@ def test_repeats_bit_for_bit_on_streams(fp4):
     assert all(torch.equal(o, want) for o in outs)
 
 
+def test_far_pages(fp4):
+    """Byte offsets past 2^32: the last pages of a cache of over 4 GiB a side."""
+    import torch
+    pages, heads, page, dim = 40000, 8, 256, 128
+    cache = fp4.KVCache.empty(pages, heads, page, dim, NV, GK, GV)
+    gen = torch.Generator().manual_seed(40)
+    table = torch.tensor([[pages - 1, 0, pages - 2], [39000, 38999, 7]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([700, 513], dtype=torch.int32, device="cuda")
+    for row in table.tolist():
+        for pg in row:
+            x = torch.randn(2, page, heads, dim, generator=gen).to(torch.bfloat16).cuda()
+            fp4.kv_append(cache, x[0], x[1], pg * page + torch.arange(page, device="cuda"))
+    check(fp4, cache, query(2, 16, dim, 41), table, lens)
+
+
+def test_workspace_contents_do_not_matter(fp4):
+    import torch
+    cache, table, n = make(fp4, NV, 128, 1, 16, 0, [3000, 5], 42)
+    q = query(2, 4, 128, 43)
+    want = fp4.paged_attention(q, cache, table, n)
+    need = fp4.paged_attention_workspace_size(2, 4, 1, 128, table.shape[1] * 16)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(fp4.paged_attention(q, cache, table, n, workspace=ws), want)
+    with pytest.raises(fp4.Fp4Error):
+        fp4.paged_attention(q, cache, table, n, workspace=ws[:need - 1])
+
+
+def test_decode_layer(fp4):
+    """One attention layer of a decode step as a server runs it, captured once
+    and replayed: the fused projection (weight-only), its keys and values into
+    the cache, attention, the output projection.  Each part is checked against
+    64 bits from the values that it was given."""
+    import torch
+    B, H, G, D, page, E = 5, 2, 4, 128, 32, 1024
+    HQ, rows = H * G, (H * G + 2 * H) * D
+    gen = torch.Generator().manual_seed(50)
+    cache, _, _ = make(fp4, NV, D, H, page, 64, [400] * B, 51)
+    table = torch.arange(B * 13, dtype=torch.int32, device="cuda").reshape(B, 13)
+    lens = torch.tensor([1, 33, 64, 400, 0], dtype=torch.int32, device="cuda")
+    slots = torch.zeros(B, dtype=torch.int64, device="cuda")
+    x = torch.zeros(B, E, dtype=torch.bfloat16, device="cuda")
+    w_in, w_out = ((torch.randn(n, k, generator=gen) * k ** -0.5).to(torch.bfloat16).cuda() for n, k in ((rows, E), (E, HQ * D)))
+    Win, Wout = fp4.quantize(w_in, MX, hadamard_k=32), fp4.quantize(w_out, NV)
+    qkv = torch.empty(B, rows, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(B, E, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(B, HQ, D, dtype=torch.bfloat16, device="cuda")
+
+    def layer():
+        fp4.linear_w4a16(x, Win, MX, hadamard_k=32, out=qkv, weights_static=True)
+        q, k, v = qkv.view(B, HQ + 2 * H, D).split((HQ, H, H), 1)
+        fp4.kv_append(cache, k, v, slots)
+        fp4.paged_attention(q, cache, table, lens, out=out)
+        fp4.linear_w4a16(out.view(B, HQ * D), Wout, NV, out=y, weights_static=True)
+
+    layer()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer()
+    for step in range(4):
+        x.copy_(torch.randn(B, E, generator=gen).to(torch.bfloat16))
+        pos = lens.long()
+        slots.copy_(table.long().gather(1, (pos // page)[:, None])[:, 0] * page + pos % page)
+        slots[4] = -1  # a padded row of the batch: no token, no length
+        lens[:4] += 1
+        g.replay()
+        torch.cuda.synchronize()
+        for got, a, W, wf, fmt, hk in ((qkv, x, Win, w_in, MX, 32), (y, out.view(B, HQ * D), Wout, w_out, NV, 0)):
+            n, kk = wf.shape
+            s = W[1][ref.atoms_index(n, kk // ref.block_of(fmt), "cuda")]
+            wv = ref.values64(W[0], s, fmt, W[2] if fmt == NV else 1.0)
+            av = ref.rotate64(a.double(), hk)
+            want, bound = av @ wv.T, av.abs() @ wv.abs().T
+            assert ((got.double() - want).abs() <= (1e-5 + (2.0**-11 if hk else 0)) * bound + 2.0**-8 * want.abs()).all()
+        q, k, v = qkv.view(B, HQ + 2 * H, D).split((HQ, H, H), 1)
+        fresh = fp4.KVCache.empty(1, H, 16, D, NV, GK, GV, 64)
+        fp4.kv_append(fresh, k.contiguous(), v.contiguous(), torch.arange(B, device="cuda"))
+        for b in range(4):
+            pg, at = int(slots[b]) // page, int(slots[b]) % page
+            for side in (0, 1):
+                assert torch.equal((cache.k, cache.v)[side][0][pg, :, at], (fresh.k, fresh.v)[side][0][0, :, b])
+        want, _, err, mag = ref.attention64(q, cache.k[0], cache.k[1], cache.v[0], cache.v[1], NV, cache.k[2], cache.v[2], 64,
+                                            table, lens, page, D ** -0.5, 0, cache.num_pages)
+        assert ((out.double() - want).abs() <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + 1e-30).all()
+        assert not out[4].any() and not y[4].any()
+
+
 def test_decode_step_captured(fp4):
     """Append and attention in one graph, replayed while the sequences grow, as
     a decode loop uses them; two graphs share one workspace in one stream."""
