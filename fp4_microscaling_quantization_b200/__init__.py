@@ -88,7 +88,15 @@ def _operand(t3, rows: int, cols: int, fmt: int, name: str, device):
     import torch
 
     q, s, g = t3
-    qb, sb = quantize_sizes(rows, cols, fmt)
+    qb, sb = _quantize_sizes(rows, cols, fmt)
+    try:  # the checks of _dev in one expression: a decode step's call takes as long as its checks
+        if (q.is_cuda and q.device == device and s.device == device and g.device == device
+                and q.dtype is torch.uint8 and s.dtype is torch.uint8 and g.dtype is torch.float32
+                and q.is_contiguous() and s.is_contiguous() and g.is_contiguous()
+                and q.nbytes >= qb and s.nbytes >= sb and g.nbytes >= 4):
+            return q, s, g
+    except AttributeError:  # not a tensor: named below
+        pass
     _dev(q, name + " elements", device, torch.uint8, qb)
     _dev(s, name + " scales", device, torch.uint8, sb)
     _dev(g, name + " tensor scale", device, torch.float32, 4)
@@ -423,26 +431,27 @@ def linear_w4a16(x, w, fmt, hadamard_k: int = 0, out_dtype: int = FP4_OUT_BF16, 
     fmt = _fmt(fmt)
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D bf16 tensor, contiguous along K")
+    device = x.device
     _dev(x, "x", None, torch.bfloat16, contiguous=False)
     M, K = x.shape
     N = w[0].shape[0]
-    Wq, Ws, gW = _operand(w, N, K, fmt, "W", x.device)
+    Wq, Ws, gW = _operand(w, N, K, fmt, "W", device)
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
+        out = x.new_empty((M, N)) if dt is torch.bfloat16 else x.new_empty((M, N), dtype=dt)
     else:
         _out2d(out, M, N, dt, "out", x.device)
-    need = _w4a16_scratch(x.device.index, M, N, K, fmt)
+    need = _w4a16_scratch(device.index, M, N, K, fmt)
     if need and workspace is None:
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     if workspace is not None:
         _dev(workspace, "workspace", x.device, torch.uint8)
-    _run("fp4_linear_w4a16", x.device,
+    _run("fp4_linear_w4a16", device,
          x.data_ptr(), M, K, x.stride(0) if M > 1 else (K + 7) // 8 * 8, fmt, int(hadamard_k),
          _opts(0, 0, 0, 0, int(bool(weights_static))),
          Wq.data_ptr(), Ws.data_ptr(), gW.data_ptr(), N, int(out_dtype), out.data_ptr(), out.stride(0) if M > 1 else N,
          workspace.data_ptr() if workspace is not None else None, workspace.numel() if workspace is not None else 0,
-         _stream_handle(torch, x.device))
+         _stream_handle(torch, device))
     return out
 
 
@@ -510,6 +519,13 @@ class KVCache:
         return cls(one(k_gscale), one(v_gscale), fmt, hadamard_k)
 
 
+def _is(t, device, dtype, shape) -> bool:
+    """Whether t is a tensor of these (all that _dev checks and the shape, in one go)."""
+    import torch
+
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype is dtype and t.shape == shape
+
+
 def _slots(slots, device):
     import torch
 
@@ -527,11 +543,12 @@ def kv_append(cache: KVCache, k, v, slots, round: int = FP4_ROUND_EVEN, mx_scale
     import torch
 
     tokens = _slots(slots, cache.device)
-    shape, ks, vs = (tokens, cache.kv_heads, cache.head_dim), k.stride(), v.stride()
-    for name, t, st in (("k", k, ks), ("v", v, vs)):
-        _dev(t, name, cache.device, torch.bfloat16, contiguous=False)
-        if t.shape != shape or (tokens and st[2] != 1):
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    for name, t in (("k", k), ("v", v)):
+        if not _is(t, cache.device, torch.bfloat16, shape) or (tokens and t.stride(2) != 1):
+            _dev(t, name, cache.device, torch.bfloat16, contiguous=False)
             raise ValueError(f"{name} must be {shape}, contiguous along its last axis")
+    ks, vs = k.stride(), v.stride()
     many, heads = tokens > 1, cache.kv_heads > 1
     _run("fp4_kv_append", cache.device,
          cache._p, k.data_ptr(), ks[0] if many else 0, ks[1] if heads else 0, v.data_ptr(), vs[0] if many else 0,
@@ -549,7 +566,7 @@ def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if out is None:
-        k, v = torch.empty((2, *shape), dtype=dt, device=cache.device).unbind(0)
+        k, v = slots.new_empty(shape, dtype=dt), slots.new_empty(shape, dtype=dt)
     else:
         k, v = out
         for name, t in (("k", k), ("v", v)):
@@ -593,15 +610,16 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
 
     dev = cache.device
     _dev(q, "q", dev, torch.bfloat16, contiguous=False)
-    qs = q.stride()
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or (q.numel() and qs[2] != 1):
+    if q.dim() != 3:
         raise ValueError(f"q must be (batch, q_heads, {cache.head_dim}), contiguous along its last axis")
-    batch, heads = q.shape[0], q.shape[1]
+    (batch, heads, dim), qs = q.shape, q.stride()
+    if dim != cache.head_dim or (batch and heads and qs[2] != 1):
+        raise ValueError(f"q must be (batch, q_heads, {cache.head_dim}), contiguous along its last axis")
     _dev(page_table, "page_table", dev, torch.int32, contiguous=False)
     if page_table.dim() != 2 or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError(f"page_table must be ({batch}, pages), contiguous along its rows")
-    _dev(seq_lens, "seq_lens", dev, torch.int32)
-    if tuple(seq_lens.shape) != (batch,):
+    if not _is(seq_lens, dev, torch.int32, (batch,)) or not seq_lens.is_contiguous():
+        _dev(seq_lens, "seq_lens", dev, torch.int32)
         raise ValueError(f"seq_lens must be ({batch},)")
     cols = page_table.shape[1]
     if max_seq_len is None:
@@ -609,7 +627,8 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     need = _attention_scratch(dev.index, batch, heads, cache.kv_heads, cache.head_dim, int(max_seq_len), int(window))
     if out is None:
-        out = torch.empty((batch, heads, cache.head_dim), dtype=dt, device=dev)
+        shape = (batch, heads, cache.head_dim)
+        out = q.new_empty(shape) if dt is torch.bfloat16 else q.new_empty(shape, dtype=dt)
     else:
         _dev(out, "out", dev, dt, batch * heads * cache.head_dim * (4 if dt == torch.float32 else 2))
     lse = torch.empty((batch, heads), dtype=torch.float32, device=dev) if return_lse else None

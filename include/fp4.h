@@ -383,7 +383,7 @@ fp4_status fp4_gemm_decode_noalloc(const uint8_t *Aq, const uint8_t *As, const f
  *             block in order (rows, not the GEMM's tiles: attention reads them
  *             with the tokens they belong to);
  *   gk, gv    NVFP4: the tensor scale of all keys, of all values (one device
- *             fp32 each, given: static for the cache's life).  Ignored for the
+ *             fp32 each, positive, given: static for the cache's life).  Ignored for the
  *             E8M0 formats, may be NULL.
  * A slot is page * page_size + position in the page.
  *   fmt         FP4_MXFP4 (block 32), FP4_NVFP4 or FP4_MXFP4_16 (block 16).
@@ -468,7 +468,8 @@ fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv
  *   out         (batch, q_heads, head_dim) contiguous, out_dtype, 16-byte aligned.
  *   lse         fp32 (batch, q_heads): log sum_t exp(scale q . k_t); may be NULL.
  *   workspace   fp4_paged_attention_workspace_size() bytes, 16-byte aligned
- *               (NULL when that is 0); contents on entry do not matter.
+ *               (NULL when that is 0); contents on entry do not matter.  Calls
+ *               that may overlap on the GPU need one each.
  * q_heads must be a multiple of kv_heads; batch and q_heads at most 65535.
  * Sums and softmax statistics are fp32; weights enter the product with V as
  * f16 (fp32 output: as two f16 terms); E8M0 scales more than 2^22 below the
@@ -497,6 +498,7 @@ fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int 
  * their row's 128 elements count as zero.  fp32 sums in a fixed order.
  *   workspace  at least fp4_linear_w4a16_workspace_size() bytes, 256-byte
  *           aligned (NULL when that is 0); its contents on entry do not matter.
+ *           Calls that may overlap on the GPU need one each.
  * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch for few rows, two
  * otherwise; results repeat bit for bit.
  */

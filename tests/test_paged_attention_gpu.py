@@ -174,6 +174,34 @@ def test_large_scores_and_tiny_queries(fp4):
     check(fp4, cache, query(1, 4, 64, 18, 3e37), table, n, scale=1e-37)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, -3.0])
+@pytest.mark.parametrize("fmt", [NV, MX])
+def test_any_scale(fp4, scale, fmt):
+    """Equal weights, scores turned over, with missing pages and a cut window."""
+    cache, table, n = make(fp4, fmt, 64, 2, 16, 0, [100, 1, 0, 1500], 60)
+    table[3, 5:9] = -1
+    check(fp4, cache, query(4, 6, 64, 61), table, n, scale=scale)
+    check(fp4, cache, query(4, 6, 64, 61), table, n, scale=scale, window=90)
+
+
+def test_empty_tables_and_batches(fp4):
+    cache, table, n = make(fp4, NV, 128, 1, 16, 0, [30, 40], 62)
+    q = query(2, 4, 128, 63)
+    out, lse = fp4.paged_attention(q, cache, table[:, :0], n, return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    out, lse = fp4.paged_attention(q, cache, table[:, :0], n, max_seq_len=100000, return_lse=True)
+    assert not out.any() and (lse == -math.inf).all()
+    assert fp4.paged_attention(q[:0], cache, table[:0], n[:0]).shape == (0, 4, 128)
+    check(fp4, cache, q, table, n, max_seq_len=1 << 20)  # a bound far above the lengths and the table
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("dim,hk,group", [(256, 16, 16), (256, 64, 3), (128, 16, 12), (64, 32, 24)])
+def test_rotations_and_wide_groups(fp4, fmt, dim, hk, group):
+    cache, table, n = make(fp4, fmt, dim, 2, 64, hk, [77, 650, 2000], 64)
+    check(fp4, cache, query(3, 2 * group, dim, 65), table, n)
+
+
 def test_far_apart_scales(fp4):
     """E8M0 scales over many binades: between tokens, and 2^20 within a row."""
     import torch
