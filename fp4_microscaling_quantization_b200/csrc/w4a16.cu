@@ -40,10 +40,11 @@ namespace w4 {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 2560;                     // bytes of a warp's step: 32 rows x 64, and the scale words
-constexpr int kStages = 4;                      // steps of a warp's ring
-constexpr int kRing = 8 * kStages * kStep;
+// Steps of a warp's ring: with more than 8 columns one less, for x.
+__host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 4 : 3; }
+__host__ __device__ constexpr int ring_of(int nt) { return 8 * stages_of(nt) * kStep; }
 constexpr int kMaxSmem = 224 * 1024;            // what a launch may ask for
-constexpr int kXBytes = 112 * 1024 - kRing;     // a stage of x: two CTAs per SM
+constexpr int x_bytes(int cols) { return 112 * 1024 - ring_of((cols + 7) / 8); }  // a stage of x: two CTAs per SM
 
 struct Args {
     const uint16_t *x;
@@ -153,7 +154,7 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
 template <int FMT, int WR, int NT, int BF16OUT>
 __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constant__ Args a)
 {
-    constexpr int WK = 8 / WR, ROWS = 32 * WR;
+    constexpr int WK = 8 / WR, ROWS = 32 * WR, kStages = stages_of(NT), kRing = ring_of(NT);
     constexpr bool NV = FMT == FP4_NVFP4;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float x_up[16];
@@ -626,11 +627,10 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
 // How a call runs: the cheaper of the two forms by a model of the time in
 // microseconds, fitted to sweeps on the B200 (N 447 .. 28672, K 448 .. 14336, M 1
 // .. 16, all formats, every tile width and cluster size: what it picks is within
-// 3 % of the best in most, 1.5 times in the worst, 30 columns of a small weight).
-// Measured, NVFP4: 14336 x 4096, M = 1: tiles of 128 rows in clusters of 2 11.5
-// us, of 64 rows alone 11.6, of 128 rows in clusters of 4 (1.5 rounds of CTAs)
-// 15.6; 28672 x 8192, M = 16: by tiles 69 us, streamed 49; 4096 x 4096, M = 16:
-// 14.4 and 23.
+// 3 % of the best on average, within a third in the worst).  Measured, NVFP4:
+// 14336 x 4096, M = 1: tiles of 128 rows in clusters of 2 11.5 us, of 64 rows
+// alone 11.5, of 128 rows in clusters of 4 (1.5 rounds of CTAs) 15.6; 28672 x
+// 8192, M = 16: by tiles 65 us, streamed 50; 4096 x 4096, M = 16: 10.4 and 23.
 struct Plan {
     int wr, cluster, slice, stage;  // by tiles: 32 * wr rows, K cut over a cluster
     bool streamed;
@@ -638,7 +638,7 @@ struct Plan {
 };
 
 // What a step costs with 16 and with 32 columns, against 8.
-static double step_factor(int cols) { return cols <= 8 ? 1.0 : cols <= 16 ? 1.42 : 3.8; }
+static double step_factor(int cols) { return cols <= 8 ? 1.0 : cols <= 16 ? 1.92 : 3.48; }
 
 static Plan plan_tiles(int64_t N, int64_t K, int cols, bool rotated, int sms)
 {
@@ -653,14 +653,14 @@ static Plan plan_tiles(int64_t N, int64_t K, int cols, bool rotated, int sms)
             if ((chunks + slice - 1) / slice != cl) continue;  // every CTA has work
             const double ctas = (double)(atoms * (4 / wr) * cl), slots = 2.0 * sms * kFill[cl];
             const double rounds = ctas / slots, whole = floor(rounds), part = rounds - whole;
-            const double turns = rounds <= 1.0 ? 1.0 : whole + (part > 0.0 ? 0.9 + 0.1 * part : 0.0);
-            const double t = (0.45 + 0.66 * std::min(1.0, ctas / (2.0 * sms))) * step_factor(cols);
-            int64_t stage = (kXBytes / cols - 64) / 256 / wk * wk;
+            const double turns = rounds <= 1.0 ? 1.0 : whole + (part > 0.0 ? 0.49 + 0.51 * part : 0.0);
+            const double t = (0.52 + 0.51 * std::min(1.0, ctas / (2.0 * sms))) * step_factor(cols);
+            int64_t stage = (x_bytes(cols) / cols - 64) / 256 / wk * wk;
             stage = std::min(std::max<int64_t>(stage, wk), (slice + wk - 1) / wk * wk);
-            // start and end, x to f16, the join of columns and CTAs, the steps, further stages of x
-            const double cost = turns * ((cl == 1 ? 2.4 : 3.5 + 0.02 * cl) + 0.018 * (rotated ? 1.6 : 1.0) * cols * (double)slice + 0.047 * cols +
-                                         0.017 * cols * (cl - 1) + t * (double)((slice + wk - 1) / wk) +
-                                         2.7 * (double)((slice + stage - 1) / stage - 1));
+            // start and end, x to f16, the join of CTAs, the steps, further stages of x
+            const double cost = turns * ((cl == 1 ? 2.35 : 3.32 + 0.03 * cl) + 0.0147 * (rotated ? 1.6 : 1.0) * cols * (double)slice +
+                                         0.03 * cols * (cl - 1) + t * (double)((slice + wk - 1) / wk) +
+                                         2.75 * (double)((slice + stage - 1) / stage - 1));
             if (best.wr == 0 || cost < best.cost) best = {wr, cl, (int)slice, (int)stage, false, cost};
         }
     }
@@ -676,7 +676,7 @@ static Plan search(int64_t N, int64_t K, int cols, bool rotated, int sms)
     if (total >= int64_t(1) << 31) return p;  // the stream's 32-bit sequence; such a weight fits no GPU
     const double grid = stream_grid(total, cols, sms);
     // two launches and x, the steps (over 16 columns: one CTA per SM), tiles cut between CTAs
-    const double cost = 10.3 + 0.34 * cols + 0.96 * (cols > 8 && cols <= 16 ? 1.42 : 1.0) * (double)total / grid + 0.17 * cols * grid / (double)tiles;
+    const double cost = 13.8 + 0.19 * cols + 0.88 * (cols > 8 && cols <= 16 ? 1.56 : 1.0) * (double)total / grid + 0.02 * cols * grid / (double)tiles;
     p.streamed = cost < p.cost;
     /*HOOK*/
     return p;
@@ -704,7 +704,7 @@ static cudaError_t launch_t(const Args &a, const Plan &p, cudaStream_t st)
     auto kern = w4a16_kernel<FMT, WR, NT, BF16OUT>;
     const size_t x = (size_t)a.cols * (a.stage * 256 + 64);
     const size_t red = (size_t)(8 / WR) * a.cols * 32 * WR * 4 + (size_t)a.M * 32 * WR * 4;
-    const size_t smem = std::max(kRing + x, red);
+    const size_t smem = std::max(ring_of(NT) + x, red);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kMaxSmem, done);
     if (e != cudaSuccess) return e;
