@@ -49,7 +49,7 @@ def _run(name: str, device, *args) -> None:
     import torch
 
     if torch._C._cuda_getDevice() == device.index:  # (the tensors' being on the GPU has initialised CUDA)
-        code = getattr(_lib.lib(), name)(*args)
+        code = getattr(_lib._lib or _lib.lib(), name)(*args)
         if code:
             _lib.check(name, code)
         return
@@ -566,7 +566,8 @@ def kv_gather(cache: KVCache, slots, out_dtype: int = FP4_OUT_BF16, out=None):
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     shape = (tokens, cache.kv_heads, cache.head_dim)
     if out is None:
-        k, v = slots.new_empty(shape, dtype=dt), slots.new_empty(shape, dtype=dt)
+        k = slots.new_empty(shape, dtype=dt)
+        v = torch.empty_like(k)
     else:
         k, v = out
         for name, t in (("k", k), ("v", v)):
@@ -627,8 +628,10 @@ def paged_attention(q, cache: KVCache, page_table, seq_lens, max_seq_len: int | 
     dt = torch.float32 if out_dtype == FP4_OUT_F32 else torch.bfloat16
     need = _attention_scratch(dev.index, batch, heads, cache.kv_heads, cache.head_dim, int(max_seq_len), int(window))
     if out is None:
-        shape = (batch, heads, cache.head_dim)
-        out = q.new_empty(shape) if dt is torch.bfloat16 else q.new_empty(shape, dtype=dt)
+        if dt is torch.bfloat16 and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            out = q.new_empty((batch, heads, dim), dtype=dt)
     else:
         _dev(out, "out", dev, dt, batch * heads * cache.head_dim * (4 if dt == torch.float32 else 2))
     lse = torch.empty((batch, heads), dtype=torch.float32, device=dev) if return_lse else None

@@ -62,6 +62,7 @@ constexpr int HT = 8;           // query heads per CTA
 constexpr float kPShift = 15.0f;  // weights are 2^15 w / w_max, inside f16's range
 constexpr int kAlign = 64;      // chunks start at multiples of the longest step
 constexpr int kMaxChunks = 1024;
+constexpr int kJoin = 256;      // threads of join_kernel
 constexpr float kTiny = 1.17549435e-38f;  // the least normal number
 
 struct Args {
@@ -196,7 +197,16 @@ FP4_DEV void write_rows(const float *o, int rows, int64_t out_row, const Args &a
             }
         }
     } else {
-        for (int i = threadIdx.x; i < rows * D; i += nt) store_out<BF16OUT>(a.out, out_row * D + i, o[i]);
+        for (int i = threadIdx.x; i < rows * D / 4; i += nt) {
+            const float4 v = reinterpret_cast<const float4 *>(o)[i];
+            if (BF16OUT) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+                reinterpret_cast<uint2 *>(a.out)[out_row * (D / 4) + i] =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+            } else {
+                reinterpret_cast<float4 *>(a.out)[out_row * (D / 4) + i] = v;
+            }
+        }
     }
 }
 
@@ -680,11 +690,11 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
 
 // Joins a row's chunks: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.
 template <int FMT, int D, int BF16OUT>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Args a)
 {
-    constexpr int LANES = D / 4, GROUPS = 128 / LANES;
+    constexpr int LANES = D / 4, GROUPS = kJoin / LANES;
     __shared__ float f[kMaxChunks];
-    __shared__ float red[8];
+    __shared__ float red[2][kJoin / 32];
     __shared__ __align__(16) float o[GROUPS][D];
     grid_dep_launch();
     grid_dep_wait();
@@ -694,25 +704,28 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     const int n = r.end > r.base ? (int)((r.end - r.base + a.chunk - 1) / a.chunk) : 0;
     const float2 *ml = a.part_ml + row * a.chunks;
     float m = -kFltMax;
-    for (int i = threadIdx.x; i < n; i += 128) {
+    for (int i = threadIdx.x; i < n; i += kJoin) {
         f[i] = ml[i].x;
         m = fmaxf(m, f[i]);
     }
 #pragma unroll
     for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    if (lane == 0) red[warp] = m;
+    if (lane == 0) red[0][warp] = m;
     __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int i = 0; i < kJoin / 32; i++) m = fmaxf(m, red[0][i]);
     float l = 0.0f;
-    for (int i = threadIdx.x; i < n; i += 128) {
+    for (int i = threadIdx.x; i < n; i += kJoin) {
         f[i] = ex2(__fsub_rn(f[i], m));
         l = __fmaf_rn(f[i], ml[i].y, l);
     }
 #pragma unroll
     for (int s = 16; s; s >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xFFFFFFFFu, l, s));
-    if (lane == 0) red[4 + warp] = l;
+    if (lane == 0) red[1][warp] = l;
     __syncthreads();
-    l = __fadd_rn(__fadd_rn(red[4], red[5]), __fadd_rn(red[6], red[7]));
+    l = red[1][0];
+#pragma unroll
+    for (int i = 1; i < kJoin / 32; i++) l = __fadd_rn(l, red[1][i]);
     const int d4 = threadIdx.x % LANES, grp = threadIdx.x / LANES;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.chunks * D) + d4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -728,7 +741,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     *reinterpret_cast<float4 *>(&o[grp][4 * d4]) = s;
     __syncthreads();
     const float gv = FMT == FP4_NVFP4 ? *a.c.gv : 1.0f;
-    for (int d = threadIdx.x; d < D; d += 128) {
+    for (int d = threadIdx.x; d < D; d += kJoin) {
         float t = o[0][d];
 #pragma unroll
         for (int k = 1; k < GROUPS; k++) t = __fadd_rn(t, o[k][d]);
@@ -737,7 +750,59 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args 
     if (a.lse && threadIdx.x == 0)
         a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
     __syncthreads();
-    write_rows<D, BF16OUT>(o[0], 1, row, a, 128);
+    write_rows<D, BF16OUT>(o[0], 1, row, a, kJoin);
+}
+
+// The same, a warp to a row: for up to 4 chunks, or very many rows, where a CTA
+// to a row is mostly its start (4096 rows of up to 4 chunks: the whole call 76.6
+// us, with 128 threads a row 80.2, with 256 85.4).  For 8 chunks of 512 rows it
+// is the other way round (48.0 and 46.2 us): a warp reads them one by one.
+constexpr int kJoinRows = 2;
+template <int FMT, int D, int BF16OUT>
+__global__ void __launch_bounds__(32 * kJoinRows) join_rows_kernel(const __grid_constant__ Args a, int64_t rows)
+{
+    constexpr int P = (D + 127) / 128;  // 16-byte pieces of a lane
+    __shared__ __align__(16) float o[kJoinRows][D];
+    grid_dep_launch();
+    grid_dep_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = (int64_t)blockIdx.x * kJoinRows, row = row0 + warp;
+    if (row < rows) {
+        const Range r = live_range(a, (int)(row / a.q_heads));
+        const int n = r.end > r.base ? (int)((r.end - r.base + a.chunk - 1) / a.chunk) : 0;
+        const float2 *ml = a.part_ml + row * a.chunks;
+        float m = -kFltMax, l = 0.0f;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i].x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        float4 s[P] = {};
+        const float4 *po = reinterpret_cast<const float4 *>(a.part_o + row * a.chunks * D) + lane;
+#pragma unroll 4
+        for (int i = 0; i < n; i++) {
+            const float2 t = ml[i];
+            const float w = ex2(__fsub_rn(t.x, m));
+            l = __fmaf_rn(w, t.y, l);
+#pragma unroll
+            for (int k = 0; k < P; k++) {
+                if (D < 128 && lane >= D / 4) continue;
+                const float4 v = po[(int64_t)i * (D / 4) + 32 * k];
+                s[k].x = __fmaf_rn(w, v.x, s[k].x);
+                s[k].y = __fmaf_rn(w, v.y, s[k].y);
+                s[k].z = __fmaf_rn(w, v.z, s[k].z);
+                s[k].w = __fmaf_rn(w, v.w, s[k].w);
+            }
+        }
+        const float norm = l == 0.0f ? 0.0f : __fdiv_rn(FMT == FP4_NVFP4 ? *a.c.gv : 1.0f, l);
+        if (a.lse && lane == 0)
+            a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
+#pragma unroll
+        for (int k = 0; k < P; k++)
+            if (D >= 128 || lane < D / 4)
+                *reinterpret_cast<float4 *>(&o[warp][4 * (lane + 32 * k)]) =
+                    make_float4(__fmul_rn(s[k].x, norm), __fmul_rn(s[k].y, norm), __fmul_rn(s[k].z, norm), __fmul_rn(s[k].w, norm));
+    }
+    __syncthreads();
+    write_rows<D, BF16OUT>(o[0], (int)(rows - row0 < kJoinRows ? rows - row0 : kJoinRows), row0, a, 32 * kJoinRows);
 }
 
 // ---------------------------------------------------------------------------
@@ -817,7 +882,10 @@ static cudaError_t launch_t(const Args &a, int64_t batch, int kv_heads, cudaStre
     if (e != cudaSuccess) return e;
     e = launch_k(kern, dim3((unsigned)(a.chunks * a.head_tiles), (unsigned)kv_heads, (unsigned)batch), dim3(NW * 32), S::SMEM, st, true, a);
     if (e != cudaSuccess || a.chunks == 1) return e;
-    return launch_k(join_kernel<FMT, D, BF16OUT>, dim3((unsigned)a.q_heads, (unsigned)batch), dim3(128), 0, st, true, a);
+    const int64_t rows = batch * a.q_heads;
+    if (a.chunks <= 4 || rows >= 2048)
+        return launch_k(join_rows_kernel<FMT, D, BF16OUT>, dim3((unsigned)((rows + kJoinRows - 1) / kJoinRows)), dim3(32 * kJoinRows), 0, st, true, a, rows);
+    return launch_k(join_kernel<FMT, D, BF16OUT>, dim3((unsigned)a.q_heads, (unsigned)batch), dim3(kJoin), 0, st, true, a);
 }
 
 template <int FMT>
