@@ -234,6 +234,16 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     const int chunk = blockIdx.x / a.head_tiles, ht = blockIdx.x - chunk * a.head_tiles;
     const int h0 = kvh * a.group + ht * HT;  // first query head
     const int nh = min(HT, a.group - ht * HT);
+    // this thread's pieces of q, asked for before anything else: the page
+    // numbers and the first pages wait for the lengths
+    constexpr int QP = D / 8, QI = (HT * QP + NW * 32 - 1) / (NW * 32);
+    uint4 q_raw[QI];
+#pragma unroll
+    for (int i = 0; i < QI; i++) {
+        const int p = i * NW * 32 + threadIdx.x, h = p / QP;
+        q_raw[i] = make_uint4(0, 0, 0, 0);
+        if (h < nh) q_raw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + b * a.q_b + (int64_t)(h0 + h) * a.q_h) + p % QP);
+    }
     const Range r = live_range(a, b);
     const int cs = r.base + chunk * a.chunk;  // below 2^31: the chunks cover max_len and less than one more
     const int ce = min(cs + a.chunk, r.end);
@@ -304,35 +314,50 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     // ---- q: rotated, times a power of two that puts its largest value in
     // [2^14, 2^15), as f16 hi + lo in 16 rows of shared memory ----
     uint16_t *qs = reinterpret_cast<uint16_t *>(smem + S::QAT);
-    for (int i = threadIdx.x; i < (HT * WPT < 32 ? 32 : HT * WPT); i += NW * 32) {  // whole warps: lanes exchange values
-        const int h = i / WPT, u = i % WPT;
-        uint4 raw[4] = {};
-        if (h < nh) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(a.q + b * a.q_b + (int64_t)(h0 + h) * a.q_h + u * 32);
 #pragma unroll
-            for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
+    for (int i = 0; i < QI; i++) {
+        const int p = i * NW * 32 + threadIdx.x, h = p / QP;  // D / 8 lanes to a head: whole warps
+        if (p >= HT * QP) break;
+        float v[8] = {bf16lo(q_raw[i].x), bf16hi(q_raw[i].x), bf16lo(q_raw[i].y), bf16hi(q_raw[i].y),
+                      bf16lo(q_raw[i].z), bf16hi(q_raw[i].z), bf16lo(q_raw[i].w), bf16hi(q_raw[i].w)};
+        if (ROT) {  // H_k: stages 1, 2, 4 here, 8 .. k / 2 between lanes, in that order
+#pragma unroll
+            for (int st = 1; st < 8; st <<= 1) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    if (e & st) continue;
+                    const float x = v[e], y = v[e + st];
+                    v[e] = __fadd_rn(x, y);
+                    v[e + st] = __fsub_rn(x, y);
+                }
+            }
+            for (int m = 1; 8 * m < a.hk; m <<= 1) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const float o = __shfl_xor_sync(0xFFFFFFFFu, v[e], m);
+                    v[e] = (lane & m) ? __fsub_rn(o, v[e]) : __fadd_rn(v[e], o);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = __fmul_rn(v[e], a.ck);
         }
-        float v[32];
-        unpack_unit(raw, v);
-        if (ROT) rotate_unit(v, a.hk, a.ck, lane);
-        float amax = absmax_tree<32>(v);
+        float amax = absmax_tree<8>(v);
 #pragma unroll
-        for (int m = 1; m < WPT; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
-        if (h >= HT) continue;
+        for (int m = 1; m < QP; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
         int e = amax > 0.0f ? (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127 - 14 : 0;
         e = e < -126 ? -126 : e;  // 2^-e stays finite
         const float down = a.scale < 0.0f ? -exp2i(-e) : exp2i(-e);  // scores times a positive factor: their order holds
-        if (u == 0) q_exp[h] = exp2i(e);
+        if (p % QP == 0) q_exp[h] = exp2i(e);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
+        for (int j = 0; j < 4; j++) {
             const float x0 = __fmul_rn(v[2 * j], down), x1 = __fmul_rn(v[2 * j + 1], down);
-            const uint32_t hi = pack_f16(x0, x1);
-            const __half2 hh = *reinterpret_cast<const __half2 *>(&hi);
-            reinterpret_cast<uint32_t *>(qs)[(h * D + u * 32) / 2 + j] = hi;
-            if (ROT)
-                reinterpret_cast<uint32_t *>(qs)[((HT + h) * D + u * 32) / 2 + j] =
-                    pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
+            hi[j] = pack_f16(x0, x1);
+            const __half2 hh = *reinterpret_cast<const __half2 *>(&hi[j]);
+            if (ROT) lo[j] = pack_f16(__fsub_rn(x0, __low2float(hh)), __fsub_rn(x1, __high2float(hh)));
         }
+        reinterpret_cast<uint4 *>(qs)[p] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (ROT) reinterpret_cast<uint4 *>(qs)[HT * QP + p] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     __syncthreads();
     uint32_t qf[2 * WPT][ROT ? 4 : 2];  // B operand, column g: hi, then lo
