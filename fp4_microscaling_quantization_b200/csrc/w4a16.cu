@@ -593,7 +593,9 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
                 else
                     place[i] = t;
             }
-            if (!whole) {
+            if (whole) {
+                __syncthreads();  // the sums are read: the next pair may end a tile too
+            } else {
                 // the last CTA to get here adds all parts, in CTA order
                 const uint32_t q = tile * (uint32_t)s.pairs;
                 const uint32_t first_cta = stream_owner(q, s), last_cta = stream_owner(q + s.pairs - 1, s);
@@ -678,7 +680,6 @@ static Plan search(int64_t N, int64_t K, int cols, bool rotated, int sms)
     // two launches and x, the steps (over 16 columns: one CTA per SM), tiles cut between CTAs
     const double cost = 13.8 + 0.19 * cols + 0.88 * (cols > 8 && cols <= 16 ? 1.56 : 1.0) * (double)total / grid + 0.02 * cols * grid / (double)tiles;
     p.streamed = cost < p.cost;
-    /*HOOK*/
     return p;
 }
 

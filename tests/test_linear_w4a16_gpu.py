@@ -197,6 +197,22 @@ def test_streamed(fp4, fmt, M, N, K, hk):
         assert torch.equal(got, want)
 
 
+# more tiles than CTAs: whole tiles that end a step after one another (K up to
+# 256: at every step), and a cut one right behind a whole one
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("M,N,K,hk", [(16, 128 * 1200 - 3, 256, 0), (12, 128 * 1100, 224, 32), (16, 128 * 400 + 1, 1024, 0), (16, 128 * 333, 1536, 128)])
+def test_streamed_whole_tiles(fp4, fmt, M, N, K, hk):
+    import torch
+    x, w = inputs(M, N, K, N + hk)
+    W = fp4.quantize(w, fmt, hadamard_k=hk)
+    before = fp4.kernel_launches()
+    fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, out_dtype=fp4.FP4_OUT_F32)
+    assert fp4.kernel_launches() - before == 2
+    want = check(fp4, x, W, fmt, hk, N)
+    for _ in range(8):
+        assert torch.equal(fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, out_dtype=fp4.FP4_OUT_F32), want)
+
+
 def test_streamed_graphs_share_a_workspace(fp4):
     """Two graphs of one stream with one workspace, replayed in turn; two
     streams at once with a workspace each."""
