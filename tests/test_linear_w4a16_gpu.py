@@ -200,7 +200,8 @@ def test_streamed(fp4, fmt, M, N, K, hk):
 # more tiles than CTAs: whole tiles that end a step after one another (K up to
 # 256: at every step), and a cut one right behind a whole one
 @pytest.mark.parametrize("fmt", [MX, NV, MX16])
-@pytest.mark.parametrize("M,N,K,hk", [(16, 128 * 1200 - 3, 256, 0), (12, 128 * 1100, 224, 32), (16, 128 * 400 + 1, 1024, 0), (16, 128 * 333, 1536, 128)])
+@pytest.mark.parametrize("M,N,K,hk", [(16, 128 * 2000 - 3, 256, 0), (14, 128 * 1000, 224, 32), (16, 128 * 800 + 1, 1024, 0),
+                                      (8, 128 * 600, 2048, 0), (16, 128 * 333, 1536, 128)])
 def test_streamed_whole_tiles(fp4, fmt, M, N, K, hk):
     import torch
     x, w = inputs(M, N, K, N + hk)
