@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     const int chunk = blockIdx.x / a.head_tiles, ht = blockIdx.x - chunk * a.head_tiles;
     const int h0 = kvh * a.group + ht * HT;  // first query head
     const int nh = min(HT, a.group - ht * HT);
+    // (plain loads: what launches before this one wrote may not be read as
+    // constant data, which no wait orders)
     // this thread's pieces of q, asked for before anything else: the page
     // numbers and the first pages wait for the lengths
     constexpr int QP = D / 8, QI = (HT * QP + NW * 32 - 1) / (NW * 32);
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     for (int i = 0; i < QI; i++) {
         const int p = i * NW * 32 + threadIdx.x, h = p / QP;
         q_raw[i] = make_uint4(0, 0, 0, 0);
-        if (h < nh) q_raw[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + b * a.q_b + (int64_t)(h0 + h) * a.q_h) + p % QP);
+        if (h < nh) q_raw[i] = reinterpret_cast<const uint4 *>(a.q + b * a.q_b + (int64_t)(h0 + h) * a.q_h)[p % QP];
     }
     const Range r = live_range(a, b);
     const int cs = r.base + chunk * a.chunk;  // below 2^31: the chunks cover max_len and less than one more
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     const int first = cs + warp * S::TS;
     constexpr int PAGED = 32 / HALVES;  // steps per batch
     auto token_at = [&](int step) { return first + (step + lane / HALVES) * (NW * S::TS) + 16 * (lane % HALVES); };
-    auto page_at = [&](int t) -> int { return t < ce ? __ldg(table + (t >> a.c.page_shift)) : -1; };
+    auto page_at = [&](int t) -> int { return t < ce ? table[t >> a.c.page_shift] : -1; };
     uint32_t row_now, bad_now;
     auto rows_of = [&](int page, int t) {
         const bool live = (uint32_t)page < (uint32_t)a.c.num_pages;  // num_pages < 2^31

@@ -55,11 +55,15 @@ FP4_DEV KvWork kv_work(uint32_t warp, int lane, int upr_shift, const FastDiv &he
     return w;
 }
 
-FP4_DEV void ldg_v8(const void *p, uint4 &a, uint4 &b)
+// Plain loads here and below: a launch may begin before the one before it has
+// ended, and no wait orders reads as constant data (ld.global.nc) of what that
+// one wrote.
+FP4_DEV void ld_v8(const void *p, uint4 &a, uint4 &b)
 {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
 }
 
 template <int FMT, int HK>
@@ -72,7 +76,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a)
     const int lane = threadIdx.x & 31;
     const KvWork w = kv_work(warp, lane, a.upr_shift, a.heads_div);
     const int only = gridDim.y == 2 ? (int)blockIdx.y : -1;  // K or V alone
-    const int64_t slot = w.token < a.tokens ? __ldg(a.slots + w.token) : -1;
+    const int64_t slot = w.token < a.tokens ? a.slots[w.token] : -1;
     const bool live = slot >= 0 && slot < a.num_slots;  // others are dropped
     uint4 raw[2][4] = {};
     if (live) {
@@ -82,11 +86,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a)
             const uint16_t *row = i ? a.v + w.token * a.v_tok + w.head * a.v_head : a.k + w.token * a.k_tok + w.head * a.k_head;
             const uint4 *p = reinterpret_cast<const uint4 *>(row + w.unit * 32);
             if (a.wide) {
-                ldg_v8(p, raw[i][0], raw[i][1]);
-                ldg_v8(p + 2, raw[i][2], raw[i][3]);
+                ld_v8(p, raw[i][0], raw[i][1]);
+                ld_v8(p + 2, raw[i][2], raw[i][3]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; e++) raw[i][e] = __ldg(p + e);
+                for (int e = 0; e < 4; e++) raw[i][e] = p[e];
             }
         }
     }
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(KvAppendArgs a)
         if (i + only == 1) continue;
         float sg = 1.0f, six_sg = 6.0f;
         if (FMT == FP4_NVFP4) {
-            sg = __ldg(i ? a.c.gv : a.c.gk);
+            sg = *(i ? a.c.gv : a.c.gk);
             six_sg = __fmul_rn(6.0f, sg);
         }
         float v[32];
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a)
     const KvWork w = kv_work(warp, lane, a.upr_shift, a.heads_div);
     const bool live = w.token < a.tokens;
     const int only = gridDim.y == 2 ? (int)blockIdx.y : -1;  // K or V alone
-    const int64_t slot = live ? __ldg(a.slots + w.token) : -1;
+    const int64_t slot = live ? a.slots[w.token] : -1;
     uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     uint32_t sb[2] = {0, 0};
     const bool held = slot >= 0 && slot < a.num_slots;  // others read as zeros
@@ -146,16 +150,16 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a)
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             if (i + only == 1) continue;
-            raw[i] = __ldg(reinterpret_cast<const uint4 *>(i ? a.c.vq : a.c.kq) + unit);
+            raw[i] = reinterpret_cast<const uint4 *>(i ? a.c.vq : a.c.kq)[unit];
             const uint8_t *s = i ? a.c.vs : a.c.ks;
-            sb[i] = (FMT == FP4_MXFP4) ? (uint32_t)__ldg(s + unit) : (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(s) + unit);
+            sb[i] = (FMT == FP4_MXFP4) ? (uint32_t)s[unit] : (uint32_t)reinterpret_cast<const uint16_t *>(s)[unit];
         }
     }
     const int64_t unit = ((w.token * a.c.heads + w.head) << a.upr_shift) + w.unit;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         if (i + only == 1) continue;
-        const float sg = (FMT == FP4_NVFP4) ? __ldg(i ? a.c.gv : a.c.gk) : 1.0f;
+        const float sg = (FMT == FP4_NVFP4) ? *(i ? a.c.gv : a.c.gk) : 1.0f;
         const uint32_t words[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         float d0, d1, v[32];
         unit_decode_factors<FMT>(sb[i], sg, d0, d1);

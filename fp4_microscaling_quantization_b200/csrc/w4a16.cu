@@ -201,12 +201,13 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
     // its one unit of x; else before it, |H x| <= sqrt(k) max |x|) ----
     const int units = (s1 - s0) * 4;  // 32-element units per row
     const bool kept = a.M * units <= kThreads && s1 - s0 <= a.stage;
+    // plain loads: what earlier launches wrote is no constant data (no wait orders that)
     auto fetch_x = [&](int m, int64_t k, float *v) {
         uint4 raw[4] = {};
         if (m < a.M && k < a.K) {
             const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + k);
 #pragma unroll
-            for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
+            for (int e = 0; e < 4; e++) raw[e] = p[e];
         }
         unpack_unit(raw, v);
     };
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
             uint32_t top = 0;
 #pragma unroll 4
             for (int i = (warp % wpr) * 32 + lane; i < pieces; i += 32 * wpr) {
-                const uint4 t = __ldg(p + i);
+                const uint4 t = p[i];
                 const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
                 for (int j = 0; j < 4; j++) top = max(top, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Ar
         if (u < real) {
             const uint4 *p = reinterpret_cast<const uint4 *>(a.x + m * a.ldx + (int64_t)u * 32);
 #pragma unroll
-            for (int e = 0; e < 4; e++) raw[e] = __ldg(p + e);
+            for (int e = 0; e < 4; e++) raw[e] = p[e];
         }
         unpack_unit(raw, v);
         rotate_unit(v, a.hk, a.ck, lane);
