@@ -24,10 +24,18 @@
 // output (2^-12 per value, below the output's own 2^-9), split into hi + lo
 // columns for fp32 output.
 //
-// Work split.  A CTA is 8 warps: WR of them side by side along N (32 rows
-// each), 8 / WR along K; a cluster of up to 8 CTAs splits K further and joins
-// its sums over distributed shared memory in a fixed order.  One launch, no
-// workspace, results repeat bit for bit.
+// Work split, two forms.  By tiles: a CTA is 8 warps, WR of them side by side
+// along N (32 rows each), 8 / WR along K, each with its own ring of asynchronous
+// copies; a cluster of up to 8 CTAs splits K further and joins its sums over
+// distributed shared memory.  One launch, no workspace; x is turned to f16 by
+// every CTA for its part of K.  Streamed, for more columns or larger weights:
+// below.  Sums have a fixed order in both: results repeat bit for bit.
+//
+// Measured (NVFP4; % of the time of W's bytes at the measured copy rate): 28672 x
+// 8192, 1 row 30.7 us (66 %; its loads alone 25.2), 8 rows 33.8, 16 rows 44.5
+// (both streamed); 14336 x 4096, 1 row 11.4 (44 %), 16 rows 20.3; 4096 x 14336,
+// 16 rows rotated by H_128 20.4, by tiles 22.2 (27.6 while a cluster's CTAs
+// stored every 8th value instead of 256 in a row).
 #include <math.h>
 
 #include <algorithm>
@@ -44,7 +52,10 @@ constexpr int kStep = 2560;                     // bytes of a warp's step: 32 ro
 __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 4 : 3; }
 __host__ __device__ constexpr int ring_of(int nt) { return 8 * stages_of(nt) * kStep; }
 constexpr int kMaxSmem = 224 * 1024;            // what a launch may ask for
-constexpr int x_bytes(int cols) { return 112 * 1024 - ring_of((cols + 7) / 8); }  // a stage of x: two CTAs per SM
+// CTAs per SM: with 32 columns one, whose sums then stay in registers (4096 x
+// 4096, 16 rotated rows to fp32: 12.3 us, with two 20.2).
+__host__ __device__ constexpr int resident(int nt) { return nt > 2 ? 1 : 2; }
+constexpr int x_bytes(int cols) { return kMaxSmem / resident((cols + 7) / 8) - ring_of((cols + 7) / 8); }  // a stage of x
 
 struct Args {
     const uint16_t *x;
@@ -152,7 +163,7 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
 }
 
 template <int FMT, int WR, int NT, int BF16OUT>
-__global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __grid_constant__ Args a)
 {
     constexpr int WK = 8 / WR, ROWS = 32 * WR, kStages = stages_of(NT), kRing = ring_of(NT);
     constexpr bool NV = FMT == FP4_NVFP4;
@@ -328,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
     if (cl > 1) cluster_sync();
     else __syncthreads();
     const float gw = NV ? *a.gw : 0.00390625f;  // e8m0_rel's 2^8
-    for (int i = threadIdx.x * cl + rank; i < a.M * ROWS; i += kThreads * cl) {
+    for (int i = rank * kThreads + threadIdx.x; i < a.M * ROWS; i += kThreads * cl) {
         const int m = i / ROWS, row = i % ROWS;
         const int64_t n = atom * 128 + (row / (8 * WR)) * 32 + (tile % (4 / WR)) * (8 * WR) + row % (8 * WR);
         float t = 0.0f;
@@ -345,11 +356,12 @@ __global__ void __launch_bounds__(kThreads, 2) w4a16_kernel(const __grid_constan
 }
 
 // ---- the streamed form -------------------------------------------------------
-// For more columns or larger weights: x is turned to f16 once (prepare_kernel,
-// into the workspace, in the order the lanes read it) instead of by every CTA,
-// and the steps of all tiles form one sequence that is cut evenly over exactly
-// the CTAs that fit on the GPU.  A tile cut between CTAs is summed by the last
-// of them to finish, in CTA order.
+// x is turned to f16 once (prepare_kernel, into the workspace, in the order the
+// lanes read it) instead of by every CTA, while the first steps of W are loaded
+// already; the steps of all tiles form one sequence that is cut evenly over
+// exactly the CTAs that fit on the GPU.  A tile cut between CTAs is summed by the
+// last of them to finish, in CTA order, 16 bytes a lane and 8 parts in flight
+// (28672 x 8192, 16 rows: 44.9 us, value by value 50).
 
 struct Stream {
     uint8_t *xh;         // [cols][pairs * 2 steps][256 bytes]
@@ -375,8 +387,10 @@ template <int BF16OUT>
 __global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s, int tiles)
 {
     __shared__ uint32_t top_w[16];
-    grid_dep_launch();
+    // In this order: stream_kernel starts when everything before this launch
+    // has ended, and reads W while x is prepared.
     grid_dep_wait();
+    grid_dep_launch();
     const int m = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = m * 512 + threadIdx.x; i < tiles; i += a.M * 512) s.counters[i] = 0;
     const int units = s.pairs * 8, real = (int)(a.K / 32);
@@ -437,7 +451,7 @@ struct StreamShape {
 };
 
 template <int FMT, int NT, int BF16OUT>
-__global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s)
+__global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s)
 {
     using S = StreamShape<NT>;
     constexpr int ST = S::ST, XG = S::XG;
@@ -505,19 +519,18 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
         const int slot = i / ((8 * NT - a.cols) * 32), p = i - slot * (8 * NT - a.cols) * 32;
         *reinterpret_cast<uint4 *>(smem + ST * WSLOT + slot * XSLOT + (a.cols + (p >> 5)) * XP + (p & 31) * 16) = make_uint4(0, 0, 0, 0);
     }
-    if (!a.w_early) grid_dep_wait();
+    // W at once: prepare_kernel let this launch begin only after its own wait
 #pragma unroll
     for (int i = 0; i < ST - 1; i++) {
         if (ln < count) {
             load_w(i);
             advance();
         }
-        if (i == 0) {  // x in the first group
-            if (a.w_early) grid_dep_wait();
-            load_x();
-        }
-        cp_async_commit();
+        if (i < ST - 2) cp_async_commit();
     }
+    grid_dep_wait();
+    load_x();  // in the last group
+    cp_async_commit();
 
     float acc[2][NT][4];
     auto clear = [&]() {
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
     int pair = (int)(begin - tile * (uint32_t)s.pairs), from = pair;
     uint32_t slot = 0;
     Piece next;
-    cp_async_wait<ST - 2>();
+    cp_async_wait<0>();  // x came last
     take(mine, next);
     for (uint32_t n = 0; n < count; n++) {
         if (n % XG == 0) {
@@ -608,11 +621,20 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
                     __threadfence();
                     const float *p0 = s.part + (int64_t)(2 * first_cta + (stream_begin(first_cta, s) < q)) * a.M * 128;
                     const float *p1 = s.part + (int64_t)(2 * first_cta + 2) * a.M * 128;  // the others begin in this tile
-                    for (int i = threadIdx.x; i < a.M * 128; i += kThreads) {
-                        float t = __ldcg(p0 + i);
-#pragma unroll 4
-                        for (uint32_t k = 0; k < last_cta - first_cta; k++) t = __fadd_rn(t, __ldcg(p1 + (int64_t)k * 2 * a.M * 128 + i));
-                        store(i, t);
+                    for (int i = threadIdx.x; i < a.M * 32; i += kThreads) {
+                        float4 t = __ldcg(reinterpret_cast<const float4 *>(p0) + i);
+#pragma unroll 8
+                        for (uint32_t k = 0; k < last_cta - first_cta; k++) {
+                            const float4 u = __ldcg(reinterpret_cast<const float4 *>(p1 + (int64_t)k * 2 * a.M * 128) + i);
+                            t.x = __fadd_rn(t.x, u.x);
+                            t.y = __fadd_rn(t.y, u.y);
+                            t.z = __fadd_rn(t.z, u.z);
+                            t.w = __fadd_rn(t.w, u.w);
+                        }
+                        store(4 * i, t.x);
+                        store(4 * i + 1, t.y);
+                        store(4 * i + 2, t.z);
+                        store(4 * i + 3, t.w);
                     }
                 }
             }
@@ -628,24 +650,25 @@ __global__ void __launch_bounds__(kThreads, NT > 2 ? 1 : 2) stream_kernel(const 
 }
 
 // How a call runs: the cheaper of the two forms by a model of the time in
-// microseconds, fitted to sweeps on the B200 (N 447 .. 28672, K 448 .. 14336, M 1
-// .. 16, all formats, every tile width and cluster size: what it picks is within
-// 3 % of the best on average, within a third in the worst).  Measured, NVFP4:
-// 14336 x 4096, M = 1: tiles of 128 rows in clusters of 2 11.5 us, of 64 rows
-// alone 11.5, of 128 rows in clusters of 4 (1.5 rounds of CTAs) 15.6; 28672 x
-// 8192, M = 16: by tiles 65 us, streamed 50; 4096 x 4096, M = 16: 10.4 and 23.
+// microseconds, fitted to sweeps on the B200 (67 shapes, N 303 .. 28672, K 256 ..
+// 28672, M 1 .. 16, all formats, every tile width and cluster size: what it picks
+// is within 4 % of the best on average, 28 % off in the worst).  Measured, NVFP4:
+// 14336 x 4096, M = 1: tiles of 64 rows 11.4 us, of 128 rows in clusters of 2
+// 11.5, in clusters of 4 (1.5 rounds of CTAs) 15.6; 28672 x 8192, M = 16: by
+// tiles 65 us, streamed 44.5; 4096 x 4096, M = 16: 10.0 and 13.3.
 struct Plan {
     int wr, cluster, slice, stage;  // by tiles: 32 * wr rows, K cut over a cluster
     bool streamed;
     double cost;
 };
 
-// What a step costs with 16 and with 32 columns, against 8.
-static double step_factor(int cols) { return cols <= 8 ? 1.0 : cols <= 16 ? 1.92 : 3.48; }
+// What a step costs with 16 columns, against 8 (32: one CTA per SM, alone at it).
+static double step_factor(int cols) { return cols <= 8 || cols > 16 ? 1.0 : 2.2; }
 
 static Plan plan_tiles(int64_t N, int64_t K, int cols, bool rotated, int sms)
 {
-    // resident CTAs: two per SM, as far as clusters of that size fill a GPC
+    const int per_sm = resident((cols + 7) / 8);
+    // resident CTAs, as far as clusters of that size fill a GPC
     static constexpr double kFill[9] = {0, 1.0, 1.0, 0.95, 0.95, 0.92, 0.89, 0.87, 0.87};
     const int64_t chunks = (K + 127) / 128, atoms = (N + 127) / 128;
     Plan best = {};
@@ -654,23 +677,23 @@ static Plan plan_tiles(int64_t N, int64_t K, int cols, bool rotated, int sms)
         for (int cl = 1; cl <= 8; cl++) {
             const int64_t slice = (chunks + cl - 1) / cl;
             if ((chunks + slice - 1) / slice != cl) continue;  // every CTA has work
-            const double ctas = (double)(atoms * (4 / wr) * cl), slots = 2.0 * sms * kFill[cl];
+            const double ctas = (double)(atoms * (4 / wr) * cl), slots = (double)per_sm * sms * kFill[cl];
             const double rounds = ctas / slots, whole = floor(rounds), part = rounds - whole;
-            const double turns = rounds <= 1.0 ? 1.0 : whole + (part > 0.0 ? 0.49 + 0.51 * part : 0.0);
-            const double t = (0.52 + 0.51 * std::min(1.0, ctas / (2.0 * sms))) * step_factor(cols);
+            const double turns = rounds <= 1.0 ? 1.0 : whole + (part > 0.0 ? 0.81 + 0.19 * part : 0.0);
+            const double t = (0.505 + 0.584 * std::min(1.0, ctas / ((double)per_sm * sms))) * step_factor(cols);
             int64_t stage = (x_bytes(cols) / cols - 64) / 256 / wk * wk;
             stage = std::min(std::max<int64_t>(stage, wk), (slice + wk - 1) / wk * wk);
             // start and end, x to f16, the join of CTAs, the steps, further stages of x
-            const double cost = turns * ((cl == 1 ? 2.35 : 3.32 + 0.03 * cl) + 0.0147 * (rotated ? 1.6 : 1.0) * cols * (double)slice +
-                                         0.03 * cols * (cl - 1) + t * (double)((slice + wk - 1) / wk) +
-                                         2.75 * (double)((slice + stage - 1) / stage - 1));
+            const double cost = turns * ((cl == 1 ? 2.06 : 2.69 + 0.021 * cl) + 0.0158 * (rotated ? 1.6 : 1.0) * cols * (double)slice +
+                                         0.0345 * cols * (cl - 1) + t * (double)((slice + wk - 1) / wk) +
+                                         2.66 * (double)((slice + stage - 1) / stage - 1));
             if (best.wr == 0 || cost < best.cost) best = {wr, cl, (int)slice, (int)stage, false, cost};
         }
     }
     return best;
 }
 
-static int stream_grid(int64_t total, int cols, int sms) { return (int)std::min<int64_t>(total, (int64_t)sms * (cols > 16 ? 1 : 2)); }
+static int stream_grid(int64_t total, int cols, int sms) { return (int)std::min<int64_t>(total, (int64_t)sms * resident((cols + 7) / 8)); }
 
 static Plan search(int64_t N, int64_t K, int cols, bool rotated, int sms)
 {
@@ -678,8 +701,8 @@ static Plan search(int64_t N, int64_t K, int cols, bool rotated, int sms)
     const int64_t tiles = (N + 127) / 128, pairs = (K + 255) / 256, total = tiles * pairs;
     if (total >= int64_t(1) << 31) return p;  // the stream's 32-bit sequence; such a weight fits no GPU
     const double grid = stream_grid(total, cols, sms);
-    // two launches and x, the steps (over 16 columns: one CTA per SM), tiles cut between CTAs
-    const double cost = 13.8 + 0.19 * cols + 0.88 * (cols > 8 && cols <= 16 ? 1.56 : 1.0) * (double)total / grid + 0.02 * cols * grid / (double)tiles;
+    // two launches and the join, x, the steps (over 16 columns: one CTA per SM)
+    const double cost = 10.3 + 0.065 * cols + 1.02 * (cols <= 8 ? 1.0 : cols <= 16 ? 1.43 : 1.29) * (double)total / grid;
     p.streamed = cost < p.cost;
     return p;
 }
