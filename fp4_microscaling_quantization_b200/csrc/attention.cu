@@ -13,10 +13,10 @@
 // token and head, and every element has to become a 16-bit operand first: the
 // issue slots of that conversion come next after HBM.  Per 32 tokens of a head
 // of 128 (4608 bytes, 198 clocks of an SM's share of HBM) a warp issues about
-// 570 instructions, 128 of them conversions (64 a clock and SM) and 128 scale
+// 600 instructions, 128 of them conversions (64 a clock and SM) and 128 scale
 // multiplies, and at 16 warps per SM about 0.6 slots of a clock are used: 67 %
-// of the measured copy rate for one sequence of 262143 tokens (MXFP4, 65.6 us),
-// 63 % for 64 of 1 to 8192 (NVFP4, 75.4 us).  So:
+// of the measured copy rate for one sequence of 262143 tokens (MXFP4, 65.3 us),
+// 63 % for 64 of 1 to 8192 (NVFP4, 75.0 us).  So:
 //   * The products run on mma.sync m16n8k16 (f16 in, fp32 sums) from registers.
 //     tcgen05 would need the dequantized tile written to shared or tensor
 //     memory first, at four times the packed bytes; its rate is not what
@@ -42,7 +42,8 @@
 //   * Every warp streams its own steps of 16, 32 or 64 tokens through its own
 //     two stages of asynchronous copies: no barrier among warps until their
 //     results are joined.  (Three or four stages, and scores computed beside
-//     the values of the step before, were no faster: 84.3 against 86.0 and 86.3.)
+//     the values of the step before, were no faster: 86.0 and 86.3 against 84.3,
+//     when that was the time of the batch above.)
 // Long sequences are cut into chunks of tokens over CTAs; a second kernel
 // joins the chunks.  The cut depends on the call's sizes only, and every sum
 // has a fixed order, so results repeat bit for bit.

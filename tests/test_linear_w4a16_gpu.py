@@ -246,6 +246,42 @@ def test_streamed_graphs_share_a_workspace(fp4):
     assert all(torch.equal(a, b) for a, b in outs)
 
 
+@pytest.mark.parametrize("M,N,K", [(8, 28003, 4096), (2, 4096, 2048)])
+def test_weight_written_by_the_launch_before(fp4, M, N, K):
+    """W quantized right before the product, into memory that the product before
+    it read as another weight: in one stream, eager and as a graph."""
+    import torch
+    sides = []
+    for seed in range(3):
+        x, w = inputs(M, N, K, 20 + seed)
+        W = fp4.quantize(w, NV)
+        sides.append((x, w, fp4.linear_w4a16(x, W, NV)))
+        torch.cuda.synchronize()
+        del W
+
+    def run():
+        outs = []
+        for _ in range(4):
+            for x, w, want in sides:
+                W = fp4.quantize(w, NV)
+                outs.append((fp4.linear_w4a16(x, W, NV), want))
+                del W
+        return outs
+
+    outs = run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for _ in range(2):
+        for a, _ in outs:
+            a.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in outs)
+
+
 @pytest.mark.parametrize("M,N,K", [(2, 256, 32768), (1, 128, 65536), (4, 130, 16384), (8, 64, 32768), (16, 40, 32768), (16, 200, 4096)])
 def test_long_slices(fp4, M, N, K):
     """Slices of x longer than the part of it that is held at a time, hi and lo
