@@ -67,6 +67,25 @@ FP4_DEV uint32_t max_byte(uint32_t w)
     return max(a, b);
 }
 
+// 2^e as a product of two factors, for any exponent that a product of two
+// numbers can have: times one and then the other is exact, unless the result
+// itself is subnormal or past the largest number.
+FP4_DEV float2 exp2_pair(int e)
+{
+    const int e0 = max(-126, min(e, 127));
+    return make_float2(exp2i(e0), exp2i(max(-126, min(e - e0, 127))));
+}
+
+// g = m 2^e with |m| in [1, 2): leaves m, returns e.  Zero, subnormal numbers,
+// infinities and NaN stay whole (e = 0).
+FP4_DEV int take_exponent(float &g)
+{
+    const uint32_t u = __float_as_uint(g), e = (u >> 23) & 0xFFu;
+    if (e == 0 || e == 255) return 0;
+    g = __uint_as_float((u & 0x807FFFFFu) | 0x3F800000u);
+    return (int)e - 127;
+}
+
 // H_k of a unit of 32 values whose neighbours in the row are in neighbouring lanes.
 FP4_DEV void rotate_unit(float *v, int hk, float ck, int lane)
 {

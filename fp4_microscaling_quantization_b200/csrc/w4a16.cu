@@ -75,6 +75,23 @@ struct Args {
     int w_early;          // W may be read before the grid-dependency wait
 };
 
+// E8M0: a step's sums are added times 2^(ref - 127 - kDown), ref the row's
+// largest scale byte; what is left of the weights' power of two is
+// 2^kRest (with e8m0_rel's 2^8).  A step's sum stays below 2^33, so scales up
+// to 2^110 keep the fp32 sums finite, down to 2^-127 the factor is exact.
+constexpr float kDown = 1.0f / (1 << 18);
+constexpr int kRest = 18 - 8;
+
+// What a row's sums are multiplied by: its power of two 2^e and that of the
+// tensor scale as one pair of factors, the scale's significand (left in gw)
+// last.  So no product on the way is larger than the result (2^e alone can be
+// 2^113).
+template <bool NV>
+FP4_DEV float2 row_factors(int e, float &gw)
+{
+    return exp2_pair(e + (NV ? take_exponent(gw) : kRest));
+}
+
 // A lane's part of a step of W: 32 elements and a scale word of 4 rows.
 struct Piece {
     uint32_t w[4][4], s[4];
@@ -150,7 +167,8 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
     if (PART) {
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            const float f0 = NV ? 1.0f : exp2i((int)ref[2 * t] - 127), f1 = NV ? 1.0f : exp2i((int)ref[2 * t + 1] - 127);
+            const float f0 = NV ? 1.0f : __fmul_rn(exp2i((int)ref[2 * t] - 127), kDown);
+            const float f1 = NV ? 1.0f : __fmul_rn(exp2i((int)ref[2 * t + 1] - 127), kDown);
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);
@@ -170,6 +188,8 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float x_up[16];
     __shared__ uint32_t x_top[16];
+    __shared__ float2 x_out[16];  // factors of the sums
+    __shared__ float w_out;
     grid_dep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -244,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + a.M * pitch + q * 64), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
         }
     };
+    float gw = NV && threadIdx.x < a.M ? *a.gw : 1.0f;
     float v[32];
     const int mine_m = threadIdx.x / units, mine_u = threadIdx.x - mine_m * units;
     if (kept) {
@@ -273,6 +294,8 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
         int e = top ? (int)(top >> 23) - 127 - (a.hk && !kept ? 10 : 14) : 0;  // below 2^15 in f16
         e = e < -126 ? -126 : e;
         x_up[threadIdx.x] = exp2i(e);
+        x_out[threadIdx.x] = row_factors<NV>(e, gw);
+        if (NV) w_out = gw;  // all of them the same
     }
 
     float acc[2][NT][4];
@@ -333,18 +356,17 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
             s = __fadd_rn(s, red[k * a.cols * ROWS + i]);
             if (a.cols > a.M) s = __fadd_rn(s, red[k * a.cols * ROWS + a.M * ROWS + i]);
         }
-        sum[i] = __fmul_rn(s, x_up[m]);
+        sum[i] = __fmul_rn(__fmul_rn(s, x_out[m].x), x_out[m].y);
     }
     const uint32_t cl = (uint32_t)a.cluster;
     if (cl > 1) cluster_sync();
     else __syncthreads();
-    const float gw = NV ? *a.gw : 0.00390625f;  // e8m0_rel's 2^8
     for (int i = rank * kThreads + threadIdx.x; i < a.M * ROWS; i += kThreads * cl) {
         const int m = i / ROWS, row = i % ROWS;
         const int64_t n = atom * 128 + (row / (8 * WR)) * 32 + (tile % (4 / WR)) * (8 * WR) + row % (8 * WR);
         float t = 0.0f;
         for (uint32_t r = 0; r < cl; r++) t = __fadd_rn(t, ld_shared_cluster_f32(mapa_shared(smem_u32(sum + i), r)));
-        t = __fmul_rn(t, gw);
+        if (NV) t = __fmul_rn(t, w_out);
         if (n < a.N) {
             if (BF16OUT)
                 static_cast<__nv_bfloat16 *>(a.out)[m * a.ldc + n] = __float2bfloat16_rn(t);
@@ -365,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
 
 struct Stream {
     uint8_t *xh;         // [cols][pairs * 2 steps][256 bytes]
-    float *x_up;         // [16]
+    float2 *x_out;       // [17]: factors of the rows' sums, then (the tensor scale's significand, -)
     unsigned *counters;  // [tiles]
     float *part;         // [2 * grid][M][128]
     int pairs;           // pairs of steps per tile
@@ -383,7 +405,7 @@ FP4_DEV uint32_t stream_owner(uint32_t q, const Stream &s)
 }
 
 // Row blockIdx.x of x: H_k, the power of two, f16 hi (and lo); also zeroes the counters.
-template <int BF16OUT>
+template <int FMT, int BF16OUT>
 __global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Args a, const __grid_constant__ Stream s, int tiles)
 {
     __shared__ uint32_t top_w[16];
@@ -393,6 +415,7 @@ __global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Ar
     grid_dep_launch();
     const int m = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = m * 512 + threadIdx.x; i < tiles; i += a.M * 512) s.counters[i] = 0;
+    float gw = FMT == FP4_NVFP4 ? *a.gw : 1.0f;
     const int units = s.pairs * 8, real = (int)(a.K / 32);
     float v[32];
     auto fetch = [&](int u) {
@@ -417,7 +440,10 @@ __global__ void __launch_bounds__(512) prepare_kernel(const __grid_constant__ Ar
     int e = top ? (int)(top >> 23) - 127 - 14 : 0;  // the largest in [2^14, 2^15)
     e = e < -126 ? -126 : e;
     const float down = exp2i(-e);
-    if (threadIdx.x == 0) s.x_up[m] = exp2i(e);
+    if (threadIdx.x == 0) {
+        s.x_out[m] = row_factors<FMT == FP4_NVFP4>(e, gw);
+        if (m == 0) s.x_out[16].x = gw;
+    }
     for (int u = threadIdx.x; u < (units + 31) / 32 * 32; u += 512) {
         if (units > 512) fetch(u);  // else v still holds the thread's one unit
         if (u >= units) continue;
@@ -460,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
     constexpr int TILES_PER_STEP = FMT == FP4_MXFP4 ? 1 : 2;  // scale tiles along K
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ unsigned arrived;
+    __shared__ float2 x_out[17];
     grid_dep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int wr = warp & 3, wk = warp >> 2, r0 = wr * 8 + g;
@@ -529,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
         if (i < ST - 2) cp_async_commit();
     }
     grid_dep_wait();
+    float2 factors = {};
+    if (threadIdx.x <= a.M) factors = s.x_out[threadIdx.x < a.M ? threadIdx.x : 16];
     load_x();  // in the last group
     cp_async_commit();
 
@@ -544,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
     int pair = (int)(begin - tile * (uint32_t)s.pairs), from = pair;
     uint32_t slot = 0;
     Piece next;
+    if (threadIdx.x <= a.M) x_out[threadIdx.x] = factors;  // (read after many barriers)
     cp_async_wait<0>();  // x came last
     take(mine, next);
     for (uint32_t n = 0; n < count; n++) {
@@ -586,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
                         if (!wk && col < a.cols) *d = __fadd_rn(acc[t][i][e], *d);
                     }
             __syncthreads();
-            const float gw = NV ? *a.gw : 0.00390625f;  // e8m0_rel's 2^8
+            const float gw = NV ? x_out[a.M].x : 1.0f;
             const bool whole = from == 0 && done;
             // a CTA has two places for parts: of a tile that its sequence begins in, of a later one
             float *place = s.part + (int64_t)(2 * blockIdx.x + (begin < tile * (uint32_t)s.pairs)) * a.M * 128;
@@ -601,7 +631,9 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
             for (int i = threadIdx.x; i < a.M * 128; i += kThreads) {
                 float t = red[i];
                 if (a.cols > a.M) t = __fadd_rn(t, red[a.M * 128 + i]);
-                t = __fmul_rn(__fmul_rn(t, s.x_up[i / 128]), gw);
+                const float2 f = x_out[i / 128];
+                t = __fmul_rn(__fmul_rn(t, f.x), f.y);
+                if (NV) t = __fmul_rn(t, gw);
                 if (whole)
                     store(i, t);
                 else
@@ -770,7 +802,7 @@ static cudaError_t launch_f(const Args &a, const Plan &p, cudaStream_t st)
 
 // Workspace of the streamed form, and its sizes.
 struct Layout {
-    size_t x_up, counters, part, total;
+    size_t x_out, counters, part, total;
     int64_t tiles;
     int pairs, grid;
 };
@@ -782,8 +814,8 @@ static Layout layout(int64_t M, int64_t N, int64_t K, int cols, int sms)
     l.pairs = (int)((K + 255) / 256);
     l.grid = stream_grid(l.tiles * l.pairs, cols, sms);
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    l.x_up = up((size_t)cols * l.pairs * 512);
-    l.counters = l.x_up + 256;
+    l.x_out = up((size_t)cols * l.pairs * 512);
+    l.counters = l.x_out + 256;
     l.part = l.counters + up((size_t)l.tiles * 4);
     l.total = l.part + (size_t)2 * l.grid * M * 128 * 4;
     return l;
@@ -796,7 +828,7 @@ static cudaError_t stream_t(const Args &a, const Stream &s, int64_t tiles, int g
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kMaxSmem, done);
     if (e != cudaSuccess) return e;
-    e = launch_k(prepare_kernel<BF16OUT>, dim3((unsigned)a.M), dim3(512), 0, st, true, a, s, (int)tiles);
+    e = launch_k(prepare_kernel<FMT, BF16OUT>, dim3((unsigned)a.M), dim3(512), 0, st, true, a, s, (int)tiles);
     if (e != cudaSuccess) return e;
     constexpr size_t smem = StreamShape<NT>::SMEM;
     return launch_k(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, true, a, s);
@@ -808,7 +840,7 @@ static cudaError_t stream_f(const Args &a, void *ws, int sms, cudaStream_t st)
     const Layout l = layout(a.M, a.N, a.K, a.cols, sms);
     uint8_t *base = static_cast<uint8_t *>(ws);
     const int share = (int)(l.tiles * l.pairs / l.grid), more = (int)(l.tiles * l.pairs % l.grid);
-    const Stream s = {base, reinterpret_cast<float *>(base + l.x_up), reinterpret_cast<unsigned *>(base + l.counters),
+    const Stream s = {base, reinterpret_cast<float2 *>(base + l.x_out), reinterpret_cast<unsigned *>(base + l.counters),
                       reinterpret_cast<float *>(base + l.part), l.pairs, share, more, make_fastdiv((uint32_t)share + 1),
                       make_fastdiv((uint32_t)share), make_fastdiv((uint32_t)l.pairs)};
     if (a.cols <= 8) return stream_t<FMT, 1, BF16OUT>(a, s, l.tiles, l.grid, st);

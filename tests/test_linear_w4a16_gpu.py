@@ -296,3 +296,67 @@ def test_empty(fp4):
     x, w = inputs(1, 128, 64, 10)
     W = fp4.quantize(w, NV)
     assert fp4.linear_w4a16(x[:0], W, NV).shape == (0, 128)
+
+
+def check_one(fp4, x, W, fmt, hk, N, f32, launches):
+    """One output type, and the form that it ran as: 1 launch by tiles, 2 streamed."""
+    import torch
+    want, bound = product64(x, W, fmt, hk, N, x.shape[1])
+    before = fp4.kernel_launches()
+    got = fp4.linear_w4a16(x, W, fmt, hadamard_k=hk, out_dtype=fp4.FP4_OUT_F32 if f32 else fp4.FP4_OUT_BF16)
+    assert fp4.kernel_launches() - before == launches
+    torch.cuda.synchronize()
+    tol = 1e-5 * bound if f32 else (1e-5 + (2.0**-11 if hk else 0)) * bound + 2.0**-8 * want.abs()
+    off = (got.double() - want).abs()
+    assert (off <= tol + 1e-30).all(), float((off / (tol + 1e-30)).max())
+
+
+# by tiles and streamed
+BOTH_FORMS = [(4, 256, 512, 1), (3, 28672, 8192, 2)]
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("hk", [0, 64])
+@pytest.mark.parametrize("M,N,K,launches", BOTH_FORMS)
+def test_results_near_the_largest(fp4, fmt, hk, M, N, K, launches):
+    """x up to 2^127, with finite results above 2^120."""
+    x, w = inputs(M, N, K, 30)
+    x[0] = 0
+    x[0, 77] = 2.0**127
+    x[1] = (x[1].double() * 2.0**116).to(x.dtype)
+    W = fp4.quantize(w, fmt, hadamard_k=hk)
+    want, _ = product64(x, W, fmt, hk, N, K)
+    assert 2.0**120 < float(want.abs().max()) < 2.0**127
+    for f32 in (True, False):
+        check_one(fp4, x, W, fmt, hk, N, f32, launches)
+
+
+@pytest.mark.parametrize("M,N,K,launches", BOTH_FORMS)
+def test_far_tensor_scales(fp4, M, N, K, launches):
+    """NVFP4 tensor scales from one end to the other, against x of the other."""
+    x, w = inputs(M, N, K, 31)
+    q, s, g = fp4.quantize(w, NV)
+    for e in (-126, -100, -10, 60, 110):
+        xs = (x.double() * 2.0 ** min(-e, 110)).to(x.dtype)
+        for f32 in (True, False):
+            check_one(fp4, xs, (q, s, g * 0 + 1.37 * 2.0**e), NV, 0, N, f32, launches)
+
+
+@pytest.mark.parametrize("fmt", [MX, MX16])
+@pytest.mark.parametrize("M,N,K,launches", BOTH_FORMS)
+def test_far_block_scales(fp4, fmt, M, N, K, launches):
+    """Rows with E8M0 scales from 2^-127 to 2^110 and x that keeps their results finite."""
+    import torch
+    x, w = inputs(M, N, K, 32)
+    W = fp4.quantize(w, fmt)
+    nkb = K // ref.block_of(fmt)
+    gen = torch.Generator().manual_seed(33)
+    s = torch.randint(0, 220, (N, 1), generator=gen) + torch.randint(0, 17, (N, nkb), generator=gen)
+    s[:9] = torch.tensor([0, 1, 2, 17, 18, 19, 22, 23, 237])[:, None]
+    W[1][ref.atoms_index(N, nkb).cuda()] = s.to(torch.uint8).cuda()
+    for e in (-20, 5, 60):  # 2^60: only rows of small scales have finite results
+        xs = (x.double() * 2.0**e).to(x.dtype)
+        want, bound = product64(xs, W, fmt, 0, N, K)
+        fine = (bound < 2.0**127).all(0)
+        got = fp4.linear_w4a16(xs, W, fmt, out_dtype=fp4.FP4_OUT_F32)
+        assert ((got.double() - want).abs() <= 1e-5 * bound + 1e-30)[:, fine].all()
