@@ -61,10 +61,20 @@ FP4_DEV uint32_t e8m0_rel(uint32_t e, uint32_t ref)
     const int t = (int)e - (int)ref + 23;
     return (uint32_t)(t > 0 ? t : 0) * 0x04000400u;
 }
-FP4_DEV uint32_t max_byte(uint32_t w)
+
+// The largest byte of a in the lower half, of b in the upper.
+FP4_DEV uint32_t max_bytes2(uint32_t a, uint32_t b)
 {
-    const uint32_t a = max(w & 0xFFu, (w >> 8) & 0xFFu), b = max((w >> 16) & 0xFFu, w >> 24);
-    return max(a, b);
+    const uint32_t x = __vmaxu2(a & 0x00FF00FFu, (a >> 8) & 0x00FF00FFu), y = __vmaxu2(b & 0x00FF00FFu, (b >> 8) & 0x00FF00FFu);
+    return __vmaxu2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+}
+
+// E8M0 bytes in the halves of a word -> what they stand for, NaN for 0xFF.
+FP4_DEV float2 e8m0x2_to_f32(uint32_t two)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"((unsigned short)__byte_perm(two, 0, 0x0020)));
+    return make_float2(bf16lo(r), bf16hi(r));
 }
 
 // 2^e as a product of two factors, for any exponent that a product of two

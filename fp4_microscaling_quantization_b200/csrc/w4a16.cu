@@ -75,10 +75,10 @@ struct Args {
     int w_early;          // W may be read before the grid-dependency wait
 };
 
-// E8M0: a step's sums are added times 2^(ref - 127 - kDown), ref the row's
-// largest scale byte; what is left of the weights' power of two is
-// 2^kRest (with e8m0_rel's 2^8).  A step's sum stays below 2^33, so scales up
-// to 2^110 keep the fp32 sums finite, down to 2^-127 the factor is exact.
+// E8M0: a step's sums are added times the row's largest scale and kDown; 2^kRest
+// is what is left (e8m0_rel's 2^8 is in the sums).  A step's sum stays below
+// 2^33, so scales up to 2^110 keep the fp32 sums finite; down to 2^-127 the
+// factor is exact.
 constexpr float kDown = 1.0f / (1 << 18);
 constexpr int kRest = 18 - 8;
 
@@ -115,12 +115,19 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
     // accumulation of many steps would not give.  Not needed for NVFP4 with
     // bf16 output: what it loses (1e-6 at K = 8192) is far below 2^-9.
     constexpr bool PART = !NV || !BF16OUT;
-    uint32_t sc[4][2], ref[4];
+    uint32_t sc[4][2], ref[2];  // ref: the largest scale bytes, of two rows each
+    if (!NV) {
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            ref[t] = max_bytes2(p.s[2 * t], p.s[2 * t + 1]);
+            if (FMT != FP4_MXFP4) ref[t] = __vmaxu2(ref[t], __shfl_xor_sync(0xFFFFFFFFu, ref[t], 2));  // the step's other scale word
+        }
+    }
 #pragma unroll
     for (int j = 0; j < 4; j++) {
+        const uint32_t top = NV ? 0 : j & 1 ? ref[j / 2] >> 16 : ref[j / 2] & 0xFFFF;
         if (FMT == FP4_MXFP4) {
-            ref[j] = max_byte(p.s[j]);
-            sc[j][0] = sc[j][1] = e8m0_rel((p.s[j] >> (8 * c)) & 0xFF, ref[j]);
+            sc[j][0] = sc[j][1] = e8m0_rel((p.s[j] >> (8 * c)) & 0xFF, top);
         } else {
             const uint32_t two = (p.s[j] >> (16 * (c & 1))) & 0xFFFF;
             if (NV) {
@@ -128,10 +135,8 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
                 sc[j][0] = __byte_perm(f, 0, 0x1010);
                 sc[j][1] = __byte_perm(f, 0, 0x3232);
             } else {
-                ref[j] = max_byte(p.s[j]);
-                ref[j] = max(ref[j], __shfl_xor_sync(0xFFFFFFFFu, ref[j], 2));  // the step's other scale word
-                sc[j][0] = e8m0_rel(two & 0xFF, ref[j]);
-                sc[j][1] = e8m0_rel(two >> 8, ref[j]);
+                sc[j][0] = e8m0_rel(two & 0xFF, top);
+                sc[j][1] = e8m0_rel(two >> 8, top);
             }
         }
     }
@@ -167,8 +172,9 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
     if (PART) {
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            const float f0 = NV ? 1.0f : __fmul_rn(exp2i((int)ref[2 * t] - 127), kDown);
-            const float f1 = NV ? 1.0f : __fmul_rn(exp2i((int)ref[2 * t + 1] - 127), kDown);
+            // (a NaN among the scales is the largest byte: the row's sum becomes NaN)
+            const float2 f = NV ? make_float2(1.0f, 1.0f) : e8m0x2_to_f32(ref[t]);
+            const float f0 = NV ? 1.0f : __fmul_rn(f.x, kDown), f1 = NV ? 1.0f : __fmul_rn(f.y, kDown);
 #pragma unroll
             for (int n = 0; n < NT; n++) {
                 acc[t][n][0] = __fmaf_rn(part[t][n][0], f0, acc[t][n][0]);

@@ -495,8 +495,9 @@ fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int 
  * Unrotated activations are taken exactly (values more than 2^28 below their
  * row's largest lose bits); rotated ones are rounded to 11 bits for bf16
  * output and to 22 for fp32.  E8M0 scales more than 2^22 below the largest of
- * their row's 128 elements count as zero, and scales may go up to 2^110.  fp32
- * sums in a fixed order; finite results stay finite whatever the powers of two
+ * their row's 128 elements count as zero, and scales may go up to 2^110; a NaN
+ * scale (E8M0 0xFF, E4M3 0x7F) makes its row's results NaN.  fp32 sums in a
+ * fixed order; finite results stay finite whatever the powers of two
  * of x and of W's tensor scale.
  *   workspace  at least fp4_linear_w4a16_workspace_size() bytes, 256-byte
  *           aligned (NULL when that is 0); its contents on entry do not matter.

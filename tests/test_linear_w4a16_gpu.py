@@ -360,3 +360,26 @@ def test_far_block_scales(fp4, fmt, M, N, K, launches):
         fine = (bound < 2.0**127).all(0)
         got = fp4.linear_w4a16(xs, W, fmt, out_dtype=fp4.FP4_OUT_F32)
         assert ((got.double() - want).abs() <= 1e-5 * bound + 1e-30)[:, fine].all()
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("M,N,K,launches", BOTH_FORMS)
+@pytest.mark.parametrize("f32", [True, False])
+def test_nan_scales_show(fp4, fmt, M, N, K, launches, f32):
+    """A NaN scale in a row of W: NaN for every row of x, and nothing else changes."""
+    import torch
+    x, w = inputs(M, N, K, 34)
+    x[0] = 0
+    W = fp4.quantize(w, fmt)
+    out = dict(out_dtype=fp4.FP4_OUT_F32 if f32 else fp4.FP4_OUT_BF16)
+    clean = fp4.linear_w4a16(x, W, fmt, **out)
+    nkb = K // ref.block_of(fmt)
+    at = ref.atoms_index(N, nkb)
+    rows = [0, 7, 31, 32, 100, 127, 128, N - 1]
+    for i, n in enumerate(rows):
+        W[1][at[n, [0, nkb - 1, 1, 5, nkb // 2][i % 5]]] = 0x7F if fmt == NV else 0xFF
+    got = fp4.linear_w4a16(x, W, fmt, **out)
+    bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+    bad[rows] = True
+    assert torch.isnan(got[:, bad]).all()
+    assert torch.equal(got[:, ~bad], clean[:, ~bad])
