@@ -150,7 +150,7 @@ FP4_DEV uint32_t v_piece(int t, int j)
     return (uint32_t)(D == 256 ? t * 128 + (j ^ (((t & 1) | (((t >> 2) & 1) << 1)) << 1)) * 16 : t * (D / 2) + j * 16);
 }
 
-// the same for two bytes, one in each half
+// e8m0_rel of two scale bytes, one in each half.
 FP4_DEV uint32_t e8m0_rel2(uint32_t e0, uint32_t e1, uint32_t ref)
 {
     const int t0 = (int)e0 - (int)ref + 23, t1 = (int)e1 - (int)ref + 23;
@@ -442,20 +442,15 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
         if (!NV) {
             // bytes as pairs of 16-bit lanes; the rows of K, then those of V
             constexpr int W = S::TS * S::SB / 4;  // words of each
+            static_assert(W % 32 == 0, "a warp's words belong to K or to V");
             uint32_t ek = 0, ev = 0;
 #pragma unroll
-            for (int i = 0; i < (2 * W + 31) / 32; i++) {
-                const int w = i * 32 + lane;
-                uint32_t q = 0;
-                if (2 * W % 32 == 0 || w < 2 * W) lds(at + 2 * S::TS * S::QB + w * 4, &q, 1);
+            for (int i = 0; i < 2 * W / 32; i++) {
+                uint32_t q;
+                lds(at + 2 * S::TS * S::QB + (i * 32 + lane) * 4, &q, 1);
                 const uint32_t e = __vmaxu2(q & 0x00FF00FFu, (q >> 8) & 0x00FF00FFu);
-                if (W % 32 == 0) {
-                    if (i * 32 < W) ek = __vmaxu2(ek, e);
-                    else ev = __vmaxu2(ev, e);
-                } else {
-                    ek = w < W ? __vmaxu2(ek, e) : ek;
-                    ev = w < W ? ev : __vmaxu2(ev, e);
-                }
+                if (i * 32 < W) ek = __vmaxu2(ek, e);
+                else ev = __vmaxu2(ev, e);
             }
             const uint32_t k2 = k_ref * 0x10001u, v2 = ref_new * 0x10001u;
             if (__any_sync(0xFFFFFFFFu, __vmaxu2(ek, k2) != k2 || __vmaxu2(ev, v2) != v2)) {
