@@ -211,6 +211,67 @@ FP4_DEV void write_rows(const float *o, int rows, int64_t out_row, const Args &a
     }
 }
 
+// What a warp has to give for the join, worked out value by value in fp32 from
+// the cache itself: its maxima, sums and unnormalised outputs of nh heads over
+// its steps of TS tokens from cs to ce.  For a warp that met an E8M0 scale of
+// 0xFF, which is NaN (of a key: its score, so all; of a value: its block's
+// channels) and which the warp's loop takes for a largest scale: no cost where
+// there is none, while a look at the bytes in the loop cost 4 to 7 % at dim 64
+// by the registers it took.  A lane holds D / 32 consecutive channels.
+template <int FMT, int D, int TS>
+__device__ __noinline__ void plain_warp(const Args &a, int b, int kvh, int h0, int nh, int cs, int ce, int begin, float *so, float *sm_m, float *sm_l)
+{
+    constexpr int E = D / 32, BLOCK = FMT == FP4_MXFP4 ? 32 : 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * E;
+    const auto values = [&](const uint8_t *q, const uint8_t *s, int64_t row, float *v) {
+        const float f = e8m0_to_f32(s[row * (D / BLOCK) + d0 / BLOCK]);
+        for (int e = 0; e < E; e += 2) {
+            e2m1x2_to_f32(q[row * (D / 2) + (d0 + e) / 2], v[e], v[e + 1]);
+            v[e] = __fmul_rn(v[e], f);
+            v[e + 1] = __fmul_rn(v[e + 1], f);
+        }
+    };
+    for (int h = 0; h < nh; h++) {
+        float q[E], o[E] = {}, m = -kFltMax, l = 0.0f;
+        for (int e = 0; e < E; e++) q[e] = bf16lo(a.q[b * a.q_b + (int64_t)(h0 + h) * a.q_h + d0 + e]);
+        if (a.hk) {
+            for (int s = 1; s < a.hk; s <<= 1) {
+                float t[E];
+                for (int e = 0; e < E; e++) {
+                    const bool up = ((d0 + e) & s) != 0;
+                    float other = s >= E ? __shfl_xor_sync(0xFFFFFFFFu, q[e], s / E) : 0.0f;
+                    for (int k = 0; s < E && k < E; k++)
+                        if (k == (e ^ s)) other = q[k];
+                    t[e] = up ? __fsub_rn(other, q[e]) : __fadd_rn(q[e], other);
+                }
+                for (int e = 0; e < E; e++) q[e] = t[e];
+            }
+            for (int e = 0; e < E; e++) q[e] = __fmul_rn(q[e], a.ck);
+        }
+        for (int t = cs; t < ce; t++) {
+            if ((t - cs) / TS % NW != warp || t < begin) continue;
+            const int page = a.table[b * a.table_b + (t >> a.c.page_shift)];
+            if ((uint32_t)page >= (uint32_t)a.c.num_pages) continue;
+            const int64_t row = kv_row(((int64_t)page << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1)), kvh, a.c);
+            float v[E], x = 0.0f;
+            values(a.c.kq, a.c.ks, row, v);
+            for (int e = 0; e < E; e++) x = __fmaf_rn(q[e], v[e], x);
+            for (int s = 1; s < 32; s <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, s));
+            x = __fmul_rn(x, a.scale);
+            const float top = fmaxf(m, x), alpha = ex2(__fsub_rn(m, top)), p = ex2(__fadd_rn(__fsub_rn(x, top), kPShift));
+            m = top;
+            l = __fmaf_rn(l, alpha, p);
+            values(a.c.vq, a.c.vs, row, v);
+            for (int e = 0; e < E; e++) o[e] = __fmaf_rn(o[e], alpha, __fmul_rn(p, v[e]));
+        }
+        if (lane == 0) {
+            sm_m[h] = m;
+            sm_l[h] = l;
+        }
+        for (int e = 0; e < E; e++) so[h * D + d0 + e] = o[e];
+    }
+}
+
 // ROT: the cache is rotated, so q has more than f16's 11 bits and its lo rows
 // are not zero (a bf16 q is exact in the hi rows alone).
 template <int FMT, int D, int BF16OUT, bool ROT>
@@ -651,19 +712,23 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with the ring
     float *so = reinterpret_cast<float *>(smem) + warp * HT * D;
-    if (g == 0) {
+    if (!NV && max(k_ref, v_ref) == 255) {
+        plain_warp<FMT, D, S::TS>(a, b, kvh, h0, nh, cs, ce, r.begin, so, sm_m[warp], sm_l[warp]);
+    } else {
+        if (g == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            sm_m[warp][2 * c + i] = m_run[i];
-            sm_l[warp][2 * c + i] = l_run[i];
+            for (int i = 0; i < 2; i++) {
+                sm_m[warp][2 * c + i] = m_run[i];
+                sm_l[warp][2 * c + i] = l_run[i];
+            }
         }
-    }
-    const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
+        const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-        const int d = g * (D / 8) + 2 * i;
-        *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
-        *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
+        for (int i = 0; i < MT; i++) {
+            const int d = g * (D / 8) + 2 * i;
+            *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
+            *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
+        }
     }
     __syncthreads();
     if (threadIdx.x < nh) {  // the rows' factors, per warp

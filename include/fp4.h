@@ -453,7 +453,10 @@ fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv
  * (window 0: from 0), in pages whose table entry lies in [0, num_pages).
  * Tokens of other entries (pages let go) take no part.  A sequence with no
  * live token gets zeros, and lse = -inf.  k and v are the cache's dequantized
- * values; what lies in a page past the length, NaN included, is not used.
+ * values; what lies in a page past the length, NaN included, is not used.  A
+ * NaN scale (E8M0 0xFF, E4M3 0x7F) of a live key makes its sequence's results
+ * NaN for the heads of that key head, one of a live value those of its block's
+ * channels.
  *   q           bf16 (batch, q_heads, head_dim), strides in elements,
  *               multiples of 8 and not negative; 16-byte aligned.
  *   page_table  device int32, batch rows of table_cols entries, row stride

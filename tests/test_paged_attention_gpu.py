@@ -381,3 +381,67 @@ def test_decode_step_captured(fp4):
                                             32, table, lens, page, D ** -0.5, 0, cache.num_pages)
         off = (out[i % 2].double() - want).abs()
         assert (off <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + 1e-30).all()
+
+
+def reference(cache, q, table, lens, scale=None, window=0):
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    return ref.attention64(q, cache.k[0], cache.k[1], cache.v[0], cache.v[1], cache.fmt, cache.k[2], cache.v[2],
+                           cache.hadamard_k, table, lens, cache.page_size, scale, window, cache.num_pages)
+
+
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_nan_scales_of_live_tokens(fp4, fmt, dim, side):
+    """One NaN scale byte of a live token.  Of a key: its score is NaN, and with
+    it every head of that key head, whatever the score's sign (both occur among
+    the heads) and wherever the token lies: alone in its sequence, alone in its
+    step, the last of many.  Of a value: NaN in its block's channels and in no
+    other.  The other sequences keep their bits."""
+    import torch
+    lens = [1, 17, 33, 65, 129, 129, 700, 64]
+    nblk = dim // ref.block_of(fmt)
+    cache, table, n = make(fp4, fmt, dim, 2, 16, 0, lens, 70, spread=1.0)
+    q = query(len(lens), 16, dim, 71)
+    q[:, 8:] = -q[:, :8]  # heads of key head 1; key head 0 gets both signs below
+    q[:, 4:8] = -q[:, :4]
+    clean = reference(cache, q, table, n)
+    for b, t in enumerate([0, 16, 32, 64, 128, 5, 699]):  # the last sequence has none
+        s = (cache.k if side == "k" else cache.v)[1]
+        s[int(table[b, t // 16]), 0, t % 16, [0, nblk - 1, nblk // 2][b % 3]] = 0x7F if fmt == NV else 0xFF
+    want, lse, err, mag = reference(cache, q, table, n)
+    assert torch.isnan(want[:7, :8]).any(-1).all() and not torch.isnan(want[:, 8:]).any() and not torch.isnan(want[7]).any()
+    got, l = fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32, return_lse=True)
+    half = fp4.paged_attention(q, cache, table, n)
+    for o in (got, half):
+        assert torch.equal(torch.isnan(o), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert ((got.double() - want).abs() <= err + 1e-30)[fine].all()
+    assert ((half.double() - want).abs() <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + 1e-30)[fine].all()
+    assert torch.equal(torch.isnan(l), torch.isnan(lse))
+    rel = (clean[2] / clean[3].clamp(min=1e-30)).amax(-1)  # as in check, of the sequences without NaN
+    ok = ~torch.isnan(lse)
+    assert ((l.double() - lse).abs()[ok] <= (rel + 2.0**-21 * (1 + lse.abs()))[ok]).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, MX16])
+@pytest.mark.parametrize("hk", [0, 32])
+@pytest.mark.parametrize("cut", [False, True])
+def test_nan_scales_rotated_and_cut(fp4, fmt, hk, cut):
+    """The same through the join of chunks and the rotation, several NaN in a sequence."""
+    import torch
+    lens = [3000, 2000]
+    cache, table, n = make(fp4, fmt, 128, 1, 16, hk, lens, 72)
+    cache.v[1].clamp_(max=120)
+    for t in (3, 900, 901, 2999):
+        cache.v[1][int(table[0, t // 16]), 0, t % 16, 1] = 0xFF
+    q = query(2, 4, 128, 73)
+    want, _, err, _ = reference(cache, q, table, n)
+    got = fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32, max_seq_len=(1 << 20) if cut else 3000)
+    assert torch.isnan(want).any() and not torch.isnan(want).all()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    fine = ~torch.isnan(want)
+    assert ((got.double() - want).abs() <= err + 1e-30)[fine].all()
+    cache.k[1][int(table[0, 1500 // 16]), 0, 1500 % 16, 2] = 0xFF
+    for o in (fp4.paged_attention(q, cache, table, n), fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32)):
+        assert torch.isnan(o[0]).all() and torch.isfinite(o[1]).all()
