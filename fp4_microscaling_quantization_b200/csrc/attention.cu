@@ -61,6 +61,9 @@ namespace attn {
 constexpr int NW = 4;           // warps per CTA, each on its own tokens
 constexpr int HT = 8;           // query heads per CTA
 constexpr float kPShift = 15.0f;  // weights are 2^15 w / w_max, inside f16's range
+// Scores (in units of log 2) from which fp32 has steps of 1: the largest
+// weight is then 2^kPShift only up to a factor of 2.
+constexpr float kFar = 8388608.0f;
 constexpr int kAlign = 64;      // chunks start at multiples of the longest step
 constexpr int kMaxChunks = 1024;
 constexpr int kJoin = 256;      // threads of join_kernel
@@ -212,25 +215,34 @@ FP4_DEV void write_rows(const float *o, int rows, int64_t out_row, const Args &a
 }
 
 // What a warp has to give for the join, worked out value by value in fp32 from
-// the cache itself: its maxima, sums and unnormalised outputs of nh heads over
-// its steps of TS tokens from cs to ce.  For a warp that met an E8M0 scale of
-// 0xFF, which is NaN (of a key: its score, so all; of a value: its block's
-// channels) and which the warp's loop takes for a largest scale: no cost where
-// there is none, while a look at the bytes in the loop cost 4 to 7 % at dim 64
-// by the registers it took.  A lane holds D / 32 consecutive channels.
+// the cache itself: its maxima, sums and unnormalised outputs of the CTA's heads
+// over its steps of TS tokens.  For what a warp's loop leaves out, at no
+// cost where it does not occur (a look at the scale bytes in the loop cost 4 to
+// 7 % at dim 64 by the registers it took), and slowly where it does:
+//   * an E8M0 scale of 0xFF, which the loop takes for a largest scale, is NaN
+//     (of a key: its score, so all; of a value: its block's channels);
+//   * scores from kFar on: the difference to the maximum, taken after the
+//     score's rounding, is 0 for the maximum itself, whatever fp32's steps.
+// A lane holds D / 32 consecutive channels.
 template <int FMT, int D, int TS>
-__device__ __noinline__ void plain_warp(const Args &a, int b, int kvh, int h0, int nh, int cs, int ce, int begin, float *so, float *sm_m, float *sm_l)
+__device__ __noinline__ void plain_warp(const Args &a, float *so, float *sm_m, float *sm_l)
 {
     constexpr int E = D / 32, BLOCK = FMT == FP4_MXFP4 ? 32 : 16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * E;
+    const int b = blockIdx.z, kvh = blockIdx.y, chunk = blockIdx.x / a.head_tiles, ht = blockIdx.x - chunk * a.head_tiles;
+    const int h0 = kvh * a.group + ht * HT, nh = min(HT, a.group - ht * HT);
+    const Range r = live_range(a, b);
+    const int cs = r.base + chunk * a.chunk, ce = min(cs + a.chunk, r.end);
     const auto values = [&](const uint8_t *q, const uint8_t *s, int64_t row, float *v) {
-        const float f = e8m0_to_f32(s[row * (D / BLOCK) + d0 / BLOCK]);
+        const uint32_t byte = s[row * (D / BLOCK) + d0 / BLOCK];
+        const float f = FMT == FP4_NVFP4 ? e4m3_to_f32(byte) : e8m0_to_f32(byte);
         for (int e = 0; e < E; e += 2) {
             e2m1x2_to_f32(q[row * (D / 2) + (d0 + e) / 2], v[e], v[e + 1]);
             v[e] = __fmul_rn(v[e], f);
             v[e + 1] = __fmul_rn(v[e + 1], f);
         }
     };
+    const float gk = FMT == FP4_NVFP4 ? *a.c.gk : 1.0f;  // (values: with the normalisation, as from the loop)
     for (int h = 0; h < nh; h++) {
         float q[E], o[E] = {}, m = -kFltMax, l = 0.0f;
         for (int e = 0; e < E; e++) q[e] = bf16lo(a.q[b * a.q_b + (int64_t)(h0 + h) * a.q_h + d0 + e]);
@@ -249,7 +261,7 @@ __device__ __noinline__ void plain_warp(const Args &a, int b, int kvh, int h0, i
             for (int e = 0; e < E; e++) q[e] = __fmul_rn(q[e], a.ck);
         }
         for (int t = cs; t < ce; t++) {
-            if ((t - cs) / TS % NW != warp || t < begin) continue;
+            if ((t - cs) / TS % NW != warp || t < r.begin) continue;
             const int page = a.table[b * a.table_b + (t >> a.c.page_shift)];
             if ((uint32_t)page >= (uint32_t)a.c.num_pages) continue;
             const int64_t row = kv_row(((int64_t)page << a.c.page_shift) + (t & ((1 << a.c.page_shift) - 1)), kvh, a.c);
@@ -257,7 +269,7 @@ __device__ __noinline__ void plain_warp(const Args &a, int b, int kvh, int h0, i
             values(a.c.kq, a.c.ks, row, v);
             for (int e = 0; e < E; e++) x = __fmaf_rn(q[e], v[e], x);
             for (int s = 1; s < 32; s <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, s));
-            x = __fmul_rn(x, a.scale);
+            x = __fmul_rn(__fmul_rn(x, gk), a.scale);
             const float top = fmaxf(m, x), alpha = ex2(__fsub_rn(m, top)), p = ex2(__fadd_rn(__fsub_rn(x, top), kPShift));
             m = top;
             l = __fmaf_rn(l, alpha, p);
@@ -705,6 +717,14 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     }
 
     // ---- join the warps ----
+    // Whether plain_warp has to work this out: a NaN scale; a maximum from kFar
+    // on; one that was passed later, whose weights past f16's range have left no
+    // finite sum.  (Asked here, beside the reductions: one sequence of 129 tokens
+    // 4.18 us, asked after them 4.22.)
+    bool plain = !NV && max(k_ref, v_ref) == 255;
+#pragma unroll
+    for (int i = 0; i < 2; i++) plain |= (fabsf(m_run[i]) >= kFar && m_run[i] != -kFltMax) || !(fabsf(acc[0][i]) <= kFltMax);
+    const bool any_plain = __any_sync(0xFFFFFFFFu, plain);
 #pragma unroll
     for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -712,23 +732,23 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with the ring
     float *so = reinterpret_cast<float *>(smem) + warp * HT * D;
-    if (!NV && max(k_ref, v_ref) == 255) {
-        plain_warp<FMT, D, S::TS>(a, b, kvh, h0, nh, cs, ce, r.begin, so, sm_m[warp], sm_l[warp]);
-    } else {
-        if (g == 0) {
+    if (g == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                sm_m[warp][2 * c + i] = m_run[i];
-                sm_l[warp][2 * c + i] = l_run[i];
-            }
+        for (int i = 0; i < 2; i++) {
+            sm_m[warp][2 * c + i] = m_run[i];
+            sm_l[warp][2 * c + i] = l_run[i];
         }
-        const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
+    }
+    const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
 #pragma unroll
-        for (int i = 0; i < MT; i++) {
-            const int d = g * (D / 8) + 2 * i;
-            *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
-            *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
-        }
+    for (int i = 0; i < MT; i++) {
+        const int d = g * (D / 8) + 2 * i;
+        *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
+        *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
+    }
+    if (any_plain) {
+        __syncwarp();  // over what was stored just now
+        plain_warp<FMT, D, S::TS>(a, so, sm_m[warp], sm_l[warp]);
     }
     __syncthreads();
     if (threadIdx.x < nh) {  // the rows' factors, per warp

@@ -445,3 +445,74 @@ def test_nan_scales_rotated_and_cut(fp4, fmt, hk, cut):
     cache.k[1][int(table[0, 1500 // 16]), 0, 1500 % 16, 2] = 0xFF
     for o in (fp4.paged_attention(q, cache, table, n), fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32)):
         assert torch.isnan(o[0]).all() and torch.isfinite(o[1]).all()
+
+
+@pytest.mark.parametrize("fmt,dim", [(NV, 128), (MX, 64), (MX16, 256)])
+@pytest.mark.parametrize("top", [1e7, 3e7, 1e8, 1e9, 1e12, 1e20, 1e30])
+def test_scores_of_any_size(fp4, fmt, dim, top):
+    """Scores far past the point where fp32 has steps of more than 1.  All keys
+    are alike but every third, which is zero: a head attends to the first kind
+    in equal shares where their score is positive, else to the second."""
+    import torch
+    lens = [1, 40, 333, 3000]
+    cache, table, n = make(fp4, fmt, dim, 1, 16, 0, lens, 77)
+    for t in cache.k[:2]:
+        t.copy_(t[0, 0, 0].expand(t.shape).clone())
+    k64 = ref.values64(cache.k[0][0, 0, 0], cache.k[1][0, 0, 0], fmt, cache.k[2])
+    for b, m in enumerate(lens):
+        for t in range(2, m, 3):
+            cache.k[0][int(table[b, t // 16]), 0, t % 16] = 0
+    q = query(4, 6, dim, 78)
+    x = q.double() @ k64
+    assert (x > 0).any() and (x < 0).any()
+    scale = float(torch.tensor(top / float(x.abs().max()), dtype=torch.float32))
+    assert float(x.abs().min()) * scale > 200.0  # the other kind's weight is below 2^-288
+    got, lse = fp4.paged_attention(q, cache, table, n, scale=scale, out_dtype=fp4.FP4_OUT_F32, return_lse=True)
+    half = fp4.paged_attention(q, cache, table, n, scale=scale)
+    for b, m in enumerate(lens):
+        for h in range(6):
+            xb = float(x[b, h]) * scale
+            t = [i for i in range(m) if (i % 3 != 2) == (xb > 0 or m == 1)]
+            top_x = xb if xb > 0 or m == 1 else 0.0
+            t = torch.tensor(t, device="cuda")
+            pg = table[b].long()[t // 16]
+            v = ref.values64(cache.v[0][pg, 0, t % 16], cache.v[1][pg, 0, t % 16], fmt, cache.v[2])
+            want, mag = v.mean(0), v.abs().mean(0)
+            # the weights are alike: additions, the split of a weight and the division remain
+            tol = (len(t) / 16 + 64) * 2.0**-22 * mag
+            assert ((got[b, h].double() - want).abs() <= tol).all()
+            assert ((half[b, h].double() - want).abs() <= tol + 2.0**-11 * mag + 2.0**-8 * want.abs()).all()
+            # the score: q in 22 bits, dim / 16 additions, scale factors; its steps in fp32 (four roundings)
+            lim = (dim / 16 + 8) * 2.0**-22 * float(q[b, h].double().abs() @ k64.abs()) * scale * (top_x != 0)
+            assert abs(float(lse[b, h]) - top_x - math.log(len(t))) <= lim + 2.0**-22 * abs(top_x) + 2.0**-20
+
+
+@pytest.mark.parametrize("fmt,dim", [(NV, 128), (MX, 64), (MX16, 256)])
+@pytest.mark.parametrize("top", [3e7, 1e9, 1e20])
+def test_far_scores_that_are_passed(fp4, fmt, dim, top):
+    """Scores of -top until the last token, whose score is 0: it takes all (for
+    the heads whose scores are +top, none)."""
+    import torch
+    lens = [130, 700, 5000]
+    cache, table, n = make(fp4, fmt, dim, 1, 16, 0, lens, 80)
+    for t in cache.k[:2]:
+        t.copy_(t[0, 0, 0].expand(t.shape).clone())
+    k64 = ref.values64(cache.k[0][0, 0, 0], cache.k[1][0, 0, 0], fmt, cache.k[2])
+    for b, m in enumerate(lens):
+        cache.k[0][int(table[b, (m - 1) // 16]), 0, (m - 1) % 16] = 0
+    q = query(3, 4, dim, 81)
+    q[:, 2:] = -q[:, :2]
+    x = q.double() @ k64
+    scale = float(torch.tensor(top / float(x.abs().max()), dtype=torch.float32))
+    assert float(x.abs().min()) * scale > 200.0
+    got = fp4.paged_attention(q, cache, table, n, scale=scale, out_dtype=fp4.FP4_OUT_F32)
+    half = fp4.paged_attention(q, cache, table, n, scale=scale)
+    for b, m in enumerate(lens):
+        for h in range(4):
+            t = torch.arange(m - 1, device="cuda") if x[b, h] > 0 else torch.tensor([m - 1], device="cuda")
+            pg = table[b].long()[t // 16]
+            v = ref.values64(cache.v[0][pg, 0, t % 16], cache.v[1][pg, 0, t % 16], fmt, cache.v[2])
+            want, mag = v.mean(0), v.abs().mean(0)
+            tol = (len(t) / 16 + 64) * 2.0**-22 * mag
+            assert ((got[b, h].double() - want).abs() <= tol).all()
+            assert ((half[b, h].double() - want).abs() <= tol + 2.0**-11 * mag + 2.0**-8 * want.abs()).all()
