@@ -61,6 +61,7 @@ namespace attn {
 constexpr int NW = 4;           // warps per CTA, each on its own tokens
 constexpr int HT = 8;           // query heads per CTA
 constexpr float kPShift = 15.0f;  // weights are 2^15 w / w_max, inside f16's range
+constexpr float kUnit = 32768.0f; // 2^kPShift: so are their sums; E8M0 outputs leave the warps without it
 // Scores (in units of log 2) from which fp32 has steps of 1: the largest
 // weight is then 2^kPShift only up to a factor of 2.
 constexpr float kFar = 8388608.0f;
@@ -270,7 +271,7 @@ __device__ __noinline__ void plain_warp(const Args &a, float *so, float *sm_m, f
             for (int e = 0; e < E; e++) x = __fmaf_rn(q[e], v[e], x);
             for (int s = 1; s < 32; s <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xFFFFFFFFu, x, s));
             x = __fmul_rn(__fmul_rn(x, gk), a.scale);
-            const float top = fmaxf(m, x), alpha = ex2(__fsub_rn(m, top)), p = ex2(__fadd_rn(__fsub_rn(x, top), kPShift));
+            const float top = fmaxf(m, x), alpha = ex2(__fsub_rn(m, top)), p = ex2(__fsub_rn(x, top));
             m = top;
             l = __fmaf_rn(l, alpha, p);
             values(a.c.vq, a.c.vs, row, v);
@@ -278,9 +279,9 @@ __device__ __noinline__ void plain_warp(const Args &a, float *so, float *sm_m, f
         }
         if (lane == 0) {
             sm_m[h] = m;
-            sm_l[h] = l;
+            sm_l[h] = __fmul_rn(l, kUnit);
         }
-        for (int e = 0; e < E; e++) so[h * D + d0 + e] = o[e];
+        for (int e = 0; e < E; e++) so[h * D + d0 + e] = FMT == FP4_NVFP4 ? __fmul_rn(o[e], kUnit) : o[e];
     }
 }
 
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
 
     // no score yet: the least finite number, so that differences stay numbers
     float m_run[2] = {-kFltMax, -kFltMax}, l_run[2] = {0.0f, 0.0f};
-    uint32_t k_ref = 0, v_ref = 0;  // E8M0: the largest scale bytes so far
+    uint32_t k_ref = 0, v_ref = 1;  // E8M0: the largest scale bytes so far
     float acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; i++) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     float x[NT / 2][4];  // 16 tokens: rows g and g + 8, heads 2c and 2c + 1 of each
     uint32_t ph[NT], pl[NT];
     constexpr int LW = (S::TS + 31) / 32;
-    uint32_t live[LW], ref_new = 0;  // a bit per token of the step, if not all take part
+    uint32_t live[LW], ref_new = 1;  // a bit per token of the step, if not all take part
     bool all = true;
 
     // Before a step's scores: which of its tokens take part; E8M0: the largest
@@ -739,7 +740,9 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
             sm_l[warp][2 * c + i] = l_run[i];
         }
     }
-    const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 0.00390625f);
+    // E8M0: without 2^15 and e8m0_rel's 2^8, so that scales up to the largest have
+    // finite sums (from 2^-126 on the factor is exact)
+    const float vf = NV ? 1.0f : __fmul_rn(exp2i((int)v_ref - 127), 1.0f / (256.0f * kUnit));
 #pragma unroll
     for (int i = 0; i < MT; i++) {
         const int d = g * (D / 8) + 2 * i;
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
         if (a.chunks > 1) {
             a.part_ml[row * a.chunks + chunk] = make_float2(m, l);
         } else {
-            norm = l == 0.0f ? 0.0f : __fdiv_rn(NV ? *a.c.gv : 1.0f, l);
+            norm = l == 0.0f ? 0.0f : __fdiv_rn(NV ? *a.c.gv : kUnit, l);
             if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
         }
 #pragma unroll
@@ -848,12 +851,12 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const __grid_constant__ Arg
     }
     *reinterpret_cast<float4 *>(&o[grp][4 * d4]) = s;
     __syncthreads();
-    const float gv = FMT == FP4_NVFP4 ? *a.c.gv : 1.0f;
+    const float gv = FMT == FP4_NVFP4 ? *a.c.gv : 1.0f, unit = FMT == FP4_NVFP4 ? l : __fmul_rn(l, 1.0f / kUnit);
     for (int d = threadIdx.x; d < D; d += kJoin) {
         float t = o[0][d];
 #pragma unroll
         for (int k = 1; k < GROUPS; k++) t = __fadd_rn(t, o[k][d]);
-        o[0][d] = l == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(t, l), gv);
+        o[0][d] = l == 0.0f ? 0.0f : __fmul_rn(__fdiv_rn(t, unit), gv);
     }
     if (a.lse && threadIdx.x == 0)
         a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_rows_kernel(const __grid_
                 s[k].w = __fmaf_rn(w, v.w, s[k].w);
             }
         }
-        const float norm = l == 0.0f ? 0.0f : __fdiv_rn(FMT == FP4_NVFP4 ? *a.c.gv : 1.0f, l);
+        const float norm = l == 0.0f ? 0.0f : __fdiv_rn(FMT == FP4_NVFP4 ? *a.c.gv : kUnit, l);
         if (a.lse && lane == 0)
             a.lse[row] = l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fsub_rn(m, kPShift), log2f(l)), 0.693147180559945f);
 #pragma unroll

@@ -474,9 +474,9 @@ fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv
  *               (NULL when that is 0); contents on entry do not matter.  Calls
  *               that may overlap on the GPU need one each.
  * q_heads must be a multiple of kv_heads; batch and q_heads at most 65535.
- * Sums and softmax statistics are fp32, scores of any size that fp32 holds are
- * taken (from 2^22 on, where fp32 has steps of 1/2 and more, slowly); weights enter the product with V as
- * f16 (fp32 output: as two f16 terms); E8M0 scales more than 2^22 below the
+ * Sums and softmax statistics are fp32; scores of any size that fp32 holds are
+ * taken (from 5.8e6 on, where fp32 has steps of 1/2, slowly).  Weights enter
+ * the product with V as f16 (fp32 output: as two f16 terms); E8M0 scales more than 2^22 below the
  * largest one of the keys (of the values) read with them count as zero.  One
  * launch, or two where long sequences are cut; results repeat bit for bit.
  */

@@ -516,3 +516,23 @@ def test_far_scores_that_are_passed(fp4, fmt, dim, top):
             tol = (len(t) / 16 + 64) * 2.0**-22 * mag
             assert ((got[b, h].double() - want).abs() <= tol).all()
             assert ((half[b, h].double() - want).abs() <= tol + 2.0**-11 * mag + 2.0**-8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("fmt", [MX, MX16])
+@pytest.mark.parametrize("length", [300, 5000])
+def test_far_value_scales(fp4, fmt, length):
+    """E8M0 scales of values from 2^-127 to 2^110, values of one sign: each
+    result is a mean of them, so it is finite."""
+    import torch
+    for lo in (0, 5, 60, 221):
+        cache, table, n = make(fp4, fmt, 64, 1, 16, 0, [length], 74)
+        cache.v[0].bitwise_and_(0x77)
+        gen = torch.Generator().manual_seed(75)
+        cache.v[1].copy_(torch.randint(lo, lo + 17, cache.v[1].shape, generator=gen).to(torch.uint8))
+        q = query(1, 4, 64, 76, 0.3)
+        want, _, err, mag = reference(cache, q, table, n)
+        got = fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32)
+        half = fp4.paged_attention(q, cache, table, n)
+        small = 2.0**-125  # results below the normal numbers
+        assert ((got.double() - want).abs() <= err + small).all()
+        assert ((half.double() - want).abs() <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + small).all()
