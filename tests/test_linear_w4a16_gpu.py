@@ -383,3 +383,17 @@ def test_nan_scales_show(fp4, fmt, M, N, K, launches, f32):
     bad[rows] = True
     assert torch.isnan(got[:, bad]).all()
     assert torch.equal(got[:, ~bad], clean[:, ~bad])
+
+
+# by tiles, with x in several parts (the slice of a CTA is longer than what it
+# holds of x at a time): 128, 64 and 32 rows to a tile, one CTA and clusters,
+# last parts of one step, K tails of 32 and 64
+@pytest.mark.parametrize("M,N,K,hk,f32", [
+    (8, 10676, 6912, 64, False), (8, 10676, 6912, 0, True), (8, 20088, 1824, 0, False), (4, 23993, 2304, 128, True),
+    (7, 4704, 11296, 0, True), (8, 2815, 14656, 0, False), (8, 9371, 5472, 0, True), (8, 65, 13344, 0, True),
+    (7, 300, 17440, 0, False), (4, 67, 14400, 64, True),
+])
+@pytest.mark.parametrize("fmt", [MX, NV, MX16])
+def test_tiles_with_x_in_parts(fp4, fmt, M, N, K, hk, f32):
+    x, w = inputs(M, N, K, M + N)
+    check_one(fp4, x, fp4.quantize(w, fmt, hadamard_k=hk), fmt, hk, N, f32, 1)
