@@ -506,8 +506,8 @@ fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int 
  *   workspace  at least fp4_linear_w4a16_workspace_size() bytes, 256-byte
  *           aligned (NULL when that is 0); its contents on entry do not matter.
  *           Calls that may overlap on the GPU need one each.
- * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch for few rows, two
- * otherwise; results repeat bit for bit.
+ * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch or two, by M, N and K
+ * (two where a workspace is needed); results repeat bit for bit.
  */
 fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
                             const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,

@@ -397,3 +397,13 @@ def test_nan_scales_show(fp4, fmt, M, N, K, launches, f32):
 def test_tiles_with_x_in_parts(fp4, fmt, M, N, K, hk, f32):
     x, w = inputs(M, N, K, M + N)
     check_one(fp4, x, fp4.quantize(w, fmt, hadamard_k=hk), fmt, hk, N, f32, 1)
+
+
+# streamed with fewer than 8 rows: columns of zeros beside the live ones
+@pytest.mark.parametrize("M,N,K,hk", [(1, 57344, 8192, 0), (1, 57344, 8192, 128), (2, 28672, 8192, 0), (3, 28672, 8224, 0),
+                                      (3, 28600, 8192, 64), (5, 14336, 14336, 0)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_streamed_few_rows(fp4, M, N, K, hk, f32):
+    for fmt in (NV, MX):
+        x, w = inputs(M, N, K, M + hk)
+        check_one(fp4, x, fp4.quantize(w, fmt, hadamard_k=hk), fmt, hk, N, f32, 2)
