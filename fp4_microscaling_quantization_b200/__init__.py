@@ -38,7 +38,11 @@ def _fmt(fmt) -> int:
 
 def _stream_handle(torch, device) -> int:
     """The current stream of a device (a tensor's, or an ordinal)."""
-    return torch._C._cuda_getCurrentRawStream(device if isinstance(device, int) else device.index)
+    index = device if isinstance(device, int) else device.index
+    # Without the stream object that the public call makes (2.2 us of a call's
+    # 10), where this torch has that.
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _run(name: str, device, *args) -> None:
@@ -48,7 +52,7 @@ def _run(name: str, device, *args) -> None:
     stream the call is given."""
     import torch
 
-    if torch._C._cuda_getDevice() == device.index:  # (the tensors' being on the GPU has initialised CUDA)
+    if torch.cuda.current_device() == device.index:
         code = getattr(_lib._lib or _lib.lib(), name)(*args)
         if code:
             _lib.check(name, code)

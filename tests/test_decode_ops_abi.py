@@ -188,3 +188,48 @@ def test_binding_refuses_host_tensors_and_shapes():
     with pytest.raises(ValueError):
         fp4.linear_w4a16(torch.zeros((2, 64), dtype=torch.bfloat16), (q, s, g), fp4.FP4_NVFP4)
     assert fp4.paged_attention_workspace_size(1, 8, 8, 64, 64) == 0
+
+
+def test_streams_without_the_private_call():
+    """A torch that lacks the raw stream call is asked by the public one; one
+    that has it, without making a stream object."""
+    from types import SimpleNamespace
+    import torch
+    import fp4_microscaling_quantization_b200 as fp4
+    asked = []
+
+    def public(device):
+        asked.append(device)
+        return SimpleNamespace(cuda_stream=77)
+
+    without = SimpleNamespace(_C=SimpleNamespace(), cuda=SimpleNamespace(current_stream=public))
+    assert fp4._stream_handle(without, torch.device("cuda", 3)) == 77 and fp4._stream_handle(without, 1) == 77
+    assert asked == [3, 1]
+    having = SimpleNamespace(_C=SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 100 + index), cuda=None)
+    assert fp4._stream_handle(having, torch.device("cuda", 3)) == 103 and fp4._stream_handle(having, 2) == 102
+
+
+def test_calls_ask_for_the_device_by_the_public_call(monkeypatch):
+    """An entry point of a device that is current runs without changing it; of
+    another device, with that one current."""
+    from contextlib import contextmanager
+    from types import SimpleNamespace
+    import torch
+    import fp4_microscaling_quantization_b200 as fp4
+    made, inside = [], []
+
+    @contextmanager
+    def device(d):
+        inside.append(d.index)
+        yield
+
+    fake = SimpleNamespace(fp4_kv_gather=lambda *a: made.append(a) or 0)
+    monkeypatch.setattr(fp4._lib, "_lib", fake)
+    monkeypatch.setattr(fp4._lib, "lib", lambda: fake)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1 / 0, raising=False)
+    fp4._run("fp4_kv_gather", torch.device("cuda", 1), 5)
+    assert made == [(5,)] and not inside
+    fp4._run("fp4_kv_gather", torch.device("cuda", 0), 6)
+    assert made == [(5,), (6,)] and inside == [0]
