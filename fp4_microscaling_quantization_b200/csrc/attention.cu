@@ -13,10 +13,11 @@
 // token and head, and every element has to become a 16-bit operand first: the
 // issue slots of that conversion come next after HBM.  Per 32 tokens of a head
 // of 128 (4608 bytes, 198 clocks of an SM's share of HBM) a warp issues about
-// 600 instructions, 128 of them conversions (64 a clock and SM) and 128 scale
-// multiplies, and at 16 warps per SM about 0.6 slots of a clock are used: 67 %
-// of the measured copy rate for one sequence of 262143 tokens (MXFP4, 65.3 us),
-// 63 % for 64 of 1 to 8192 (NVFP4, 75.0 us).  So:
+// 630 instructions, 128 of them conversions (64 a clock and SM) and 128 scale
+// multiplies, and at 16 warps per SM about 0.6 slots of a clock are used: 66 %
+// of the measured copy rate for one sequence of 262143 tokens (MXFP4, 66.0 us
+// in a graph of calls, as all times here), 62 % for 64 of 1 to 8192 (NVFP4,
+// 76.2 us).  So:
 //   * The products run on mma.sync m16n8k16 (f16 in, fp32 sums) from registers.
 //     tcgen05 would need the dequantized tile written to shared or tensor
 //     memory first, at four times the packed bytes; its rate is not what

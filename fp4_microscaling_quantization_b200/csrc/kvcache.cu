@@ -15,9 +15,12 @@
 // warp 5.1).  A warp owns 32 / (dim / 32)
 // consecutive tokens of one head: with consecutive slots its nibbles are 512
 // contiguous bytes of a page, and its bf16 rows are whole 2 * dim byte
-// segments, read and written 32 bytes a lane.  Bound: HBM for prompts, at 64
-// and 128 the rotation's issue slots; the launch and two dependent loads
-// (slot, then data) for a decode step.
+// segments, read and written 32 bytes a lane.  Bound: HBM for prompts (100003
+// tokens read back at 99 % of the measured copy rate); with H_64 68 %, where
+// most of a warp's time is the wait for its loads (long_scoreboard 2.9 and 3.3
+// per issue at 7 warps per scheduler, 0.65 of the issue slots used): a thread
+// loads, computes and stores once.  The launch and two dependent loads (slot,
+// then data) for a decode step.
 #include "frag.cuh"
 #include "kv.cuh"
 #include "sm100.cuh"

@@ -21,7 +21,7 @@
 // it count as zero).  x in f16 is a power of two (per row and K slice, the
 // largest value in [2^14, 2^15)) times its bf16 value: exact down to 2^-28 of
 // the largest.  After a rotation x has 24 bits: rounded to f16's 11 for bf16
-// output (2^-12 per value, below the output's own 2^-9), split into hi + lo
+// output (2^-11 per value, below the output's own 2^-8), split into hi + lo
 // columns for fp32 output.
 //
 // Work split, two forms.  By tiles: a CTA is 8 warps, WR of them side by side
@@ -31,11 +31,11 @@
 // every CTA for its part of K.  Streamed, for more columns or larger weights:
 // below.  Sums have a fixed order in both: results repeat bit for bit.
 //
-// Measured (NVFP4; % of the time of W's bytes at the measured copy rate): 28672 x
-// 8192, 1 row 30.7 us (66 %; its loads alone 25.2), 8 rows 33.8, 16 rows 44.5
-// (both streamed); 14336 x 4096, 1 row 11.4 (44 %), 16 rows 20.3; 4096 x 14336,
-// 16 rows rotated by H_128 20.4, by tiles 22.2 (27.6 while a cluster's CTAs
-// stored every 8th value instead of 256 in a row).
+// Measured (NVFP4, a graph of calls; % of the time of W's bytes at the measured
+// copy rate): 28672 x 8192, 1 row to fp32 30.8 us (66 %; its loads alone 25.2),
+// 8 rows 33.5, 16 rows 44.1 (both streamed); 14336 x 4096, 1 row 11.6 (44 %),
+// 16 rows 19.8; 4096 x 14336, 16 rows rotated by H_128 20.0, by tiles 22.2 (27.6
+// while a cluster's CTAs stored every 8th value instead of 256 in a row).
 #include <math.h>
 
 #include <algorithm>
@@ -53,7 +53,7 @@ __host__ __device__ constexpr int stages_of(int nt) { return nt == 1 ? 4 : 3; }
 __host__ __device__ constexpr int ring_of(int nt) { return 8 * stages_of(nt) * kStep; }
 constexpr int kMaxSmem = 224 * 1024;            // what a launch may ask for
 // CTAs per SM: with 32 columns one, whose sums then stay in registers (4096 x
-// 4096, 16 rotated rows to fp32: 12.3 us, with two 20.2).
+// 4096, 16 rotated rows to fp32: 12.4 us, with two 20.2).
 __host__ __device__ constexpr int resident(int nt) { return nt > 2 ? 1 : 2; }
 constexpr int x_bytes(int cols) { return kMaxSmem / resident((cols + 7) / 8) - ring_of((cols + 7) / 8); }  // a stage of x
 
@@ -113,7 +113,7 @@ FP4_DEV void multiply_step(const Piece &p, uint32_t xb, uint32_t pitch, int cols
     constexpr bool NV = FMT == FP4_NVFP4;
     // The step's own sums, added with a rounding to nearest, which the product's
     // accumulation of many steps would not give.  Not needed for NVFP4 with
-    // bf16 output: what it loses (1e-6 at K = 8192) is far below 2^-9.
+    // bf16 output: what it loses (1e-6 at K = 8192) is far below 2^-8.
     constexpr bool PART = !NV || !BF16OUT;
     uint32_t sc[4][2], ref[2];  // ref: the largest scale bytes, of two rows each
     if (!NV) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) w4a16_kernel(const __g
 // already; the steps of all tiles form one sequence that is cut evenly over
 // exactly the CTAs that fit on the GPU.  A tile cut between CTAs is summed by the
 // last of them to finish, in CTA order, 16 bytes a lane and 8 parts in flight
-// (28672 x 8192, 16 rows: 44.9 us, value by value 50).
+// (28672 x 8192, 16 rows: 44.1 us; value by value it was 50).
 
 struct Stream {
     uint8_t *xh;         // [cols][pairs * 2 steps][256 bytes]
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, resident(NT)) stream_kernel(const __
 // is within 4 % of the best on average, 28 % off in the worst).  Measured, NVFP4:
 // 14336 x 4096, M = 1: tiles of 64 rows 11.4 us, of 128 rows in clusters of 2
 // 11.5, in clusters of 4 (1.5 rounds of CTAs) 15.6; 28672 x 8192, M = 16: by
-// tiles 65 us, streamed 44.5; 4096 x 4096, M = 16: 10.0 and 13.3.
+// tiles 65 us, streamed 44.1; 4096 x 4096, M = 16: 10.0 and 13.3.
 struct Plan {
     int wr, cluster, slice, stage;  // by tiles: 32 * wr rows, K cut over a cluster
     bool streamed;

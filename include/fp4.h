@@ -467,6 +467,7 @@ fp4_status fp4_paged_attention_workspace_size(int64_t batch, int q_heads, int kv
  *               table_cols * page_size is taken as the smaller of these, a
  *               negative one as 0.
  *   max_seq_len host bound of the lengths: it sizes the work split (1 .. 2^30).
+ *               The closer it is to the longest length, the faster the call.
  *   scale       times the scores, 1/sqrt(head_dim) in most models.
  *   out         (batch, q_heads, head_dim) contiguous, out_dtype, 16-byte aligned.
  *   lse         fp32 (batch, q_heads): log sum_t exp(scale q . k_t); may be NULL.
@@ -506,8 +507,8 @@ fp4_status fp4_linear_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int 
  *   workspace  at least fp4_linear_w4a16_workspace_size() bytes, 256-byte
  *           aligned (NULL when that is 0); its contents on entry do not matter.
  *           Calls that may overlap on the GPU need one each.
- * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch or two, by M, N and K
- * (two where a workspace is needed); results repeat bit for bit.
+ * M > 16 or K == 0: FP4_ERR_UNSUPPORTED.  One launch or two, by M, N, K and
+ * the rotation; results repeat bit for bit.
  */
 fp4_status fp4_linear_w4a16(const void *x, int64_t M, int64_t K, int64_t ld_x, int fmt, int hadamard_k,
                             const fp4_opts *opts, const uint8_t *Wq, const uint8_t *Ws, const float *gW, int64_t N,
