@@ -721,11 +721,12 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
     // ---- join the warps ----
     // Whether plain_warp has to work this out: a NaN scale; a maximum from kFar
     // on; one that was passed later, whose weights past f16's range have left no
-    // finite sum.  (Asked here, beside the reductions: one sequence of 129 tokens
-    // 4.18 us, asked after them 4.22.)
+    // finite outputs, though there is a sum (of queries that are NaN there is
+    // none, and the result is right).
     bool plain = !NV && max(k_ref, v_ref) == 255;
 #pragma unroll
-    for (int i = 0; i < 2; i++) plain |= (fabsf(m_run[i]) >= kFar && m_run[i] != -kFltMax) || !(fabsf(acc[0][i]) <= kFltMax);
+    for (int i = 0; i < 2; i++)
+        plain |= (fabsf(m_run[i]) >= kFar && fabsf(m_run[i]) < kFltMax) || (l_run[i] > 0.0f && !(fabsf(acc[0][i]) <= kFltMax));
     const bool any_plain = __any_sync(0xFFFFFFFFu, plain);
 #pragma unroll
     for (int i = 0; i < 2; i++)
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(NW * 32, D == 256 ? (ROT ? 2 : 3) : 4) paged_k
         *reinterpret_cast<float2 *>(so + (2 * c) * D + d) = make_float2(__fmul_rn(acc[i][0], vf), __fmul_rn(acc[i][2], vf));
         *reinterpret_cast<float2 *>(so + (2 * c + 1) * D + d) = make_float2(__fmul_rn(acc[i][1], vf), __fmul_rn(acc[i][3], vf));
     }
-    if (any_plain) {
+    if (__builtin_expect(any_plain, 0)) {
         __syncwarp();  // over what was stored just now
         plain_warp<FMT, D, S::TS>(a, so, sm_m[warp], sm_l[warp]);
     }

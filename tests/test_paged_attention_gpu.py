@@ -536,3 +536,24 @@ def test_far_value_scales(fp4, fmt, length):
         small = 2.0**-125  # results below the normal numbers
         assert ((got.double() - want).abs() <= err + small).all()
         assert ((half.double() - want).abs() <= err + 2.0**-11 * mag + 2.0**-8 * want.abs() + small).all()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("fmt,dim,hk", [(NV, 128, 0), (MX, 64, 64), (MX16, 256, 0)])
+def test_queries_that_are_not_finite(fp4, fmt, dim, hk, value):
+    """NaN for that head of that sequence, every other row keeps its bits."""
+    import torch
+    lens = [1, 40, 600, 3000]
+    cache, table, n = make(fp4, fmt, dim, 2, 16, hk, lens, 90)
+    q = query(4, 6, dim, 91)
+    cache.k[0][:, 0, :, 0] &= 0x0F  # element 1 of every key is 0: 0 * inf is NaN
+    ref_out, ref_lse = fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32, return_lse=True)
+    bad = torch.zeros(4, 6, dtype=torch.bool, device="cuda")
+    bad[:, 1] = True
+    bad[2, 0] = True
+    q[:, 1, 1] = value
+    q[2, 0, 1] = value
+    got, l = fp4.paged_attention(q, cache, table, n, out_dtype=fp4.FP4_OUT_F32, return_lse=True)
+    half = fp4.paged_attention(q, cache, table, n)
+    assert torch.isnan(got[bad]).all() and torch.isnan(half[bad]).all() and torch.isnan(l[bad]).all()
+    assert torch.equal(got[~bad], ref_out[~bad]) and torch.equal(l[~bad], ref_lse[~bad]) and torch.isfinite(half[~bad]).all()
